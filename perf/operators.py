@@ -1,0 +1,488 @@
+"""Cases of the block-of-128 FP8 operators and of the AdamW step, with their plain forms.
+
+Three operators of one training or serving step:
+
+  quantize  a matrix to FP8 codes with one power-of-two (E8M0) scale per 1 x 128 or
+            128 x 128 block, in its own orientation, transposed, or both
+  gemm      D = deq(A) deq(B) (+ C) of such operands
+  adamw     one AdamW step over many tensors, with FP32 states or with FP8 states that
+            hold one E8M0 scale per 128 elements and are rounded stochastically
+
+With ``own`` false, ``run`` computes them from elementary torch operations; with it
+true, through the package's entry points.
+"""
+import itertools
+import math
+
+import torch
+
+own = False
+
+FP8 = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+DEV = "cuda"
+
+
+# ----------------------------------------------------------------------------------------
+# Cases
+# ----------------------------------------------------------------------------------------
+def listed():
+    q = dict(op="quantize")
+    g = dict(op="gemm", alpha=1.0)
+    w = dict(op="adamw", lr=1e-4, weight_decay=0.1)
+    return [
+        # the activations of 16 decoded tokens, ahead of every projection: latency
+        dict(q, name="quantize_16x8192", rows=16, k=8192, type="bf16", fmt="e4m3", block_rows=1,
+             want="rows"),
+        # a training batch's activations: rows for the forward product, the transpose for
+        # the weight gradient, from one read
+        dict(q, name="quantize_act_16384x4096", rows=16384, k=4096, type="bf16", fmt="e4m3",
+             block_rows=1, want="both"),
+        # an FP32 master weight after the optimizer step, for the forward product and, transposed, for
+        # the input gradient
+        dict(q, name="quantize_weight_14336x4096", rows=14336, k=4096, type="f32", fmt="e4m3",
+             block_rows=128, want="both"),
+        # 16 decoded tokens against one weight: streams the weight
+        dict(g, name="gemm_decode_16x8192x8192", M=16, N=8192, K=8192, a_fmt="e4m3", b_fmt="e4m3",
+             a_block_rows=1, b_block_rows=128, out="bf16", accumulate=False),
+        # one decoded token and a small projection: the smallest call
+        dict(g, name="gemm_decode_1x1024x4096", M=1, N=1024, K=4096, a_fmt="e4m3", b_fmt="e4m3",
+             a_block_rows=1, b_block_rows=128, out="bf16", accumulate=False),
+        # a prompt of odd length, sizes that leave partial tiles and a partial K block
+        dict(g, name="gemm_prompt_1111x4000x4064", M=1111, N=4000, K=4064, a_fmt="e4m3",
+             b_fmt="e4m3", a_block_rows=1, b_block_rows=128, out="bf16", accumulate=False),
+        # the feed-forward product of a training batch
+        dict(g, name="gemm_ffn_16384x14336x4096", M=16384, N=14336, K=4096, a_fmt="e4m3",
+             b_fmt="e4m3", a_block_rows=1, b_block_rows=128, out="bf16", accumulate=False),
+        # a weight gradient: both operands scaled along the tokens, added to the FP32 gradient
+        dict(g, name="gemm_dw_4096x4096x16384", M=4096, N=4096, K=16384, a_fmt="e5m2",
+             b_fmt="e4m3", a_block_rows=1, b_block_rows=1, out="f32", accumulate=True),
+        # norms and biases of a few layers, FP32 states: latency
+        dict(w, name="adamw_f32_small", sizes="4096,4096,128,128,14336,1,8192,1000", state="f32",
+             p_type="f32", g_type="f32", step=10),
+        # the three feed-forward weights of a layer and its norms, FP32 states and gradients
+        dict(w, name="adamw_f32_layer", sizes="58720256,58720256,58720256,4096,4096", state="f32",
+             p_type="f32", g_type="f32", step=1000),
+        # the same with FP8 states and bf16 gradients
+        dict(w, name="adamw_fp8_layer", sizes="58720256,58720256,58720256,4096,4096", state="fp8",
+             p_type="f32", g_type="bf16", step=1000),
+        # odd sizes, bf16 parameters without a master copy, FP8 states
+        dict(w, name="adamw_fp8_ragged", sizes="1000003,77777,129,127,128,5,300000,1", state="fp8",
+             p_type="bf16", g_type="bf16", step=3),
+    ]
+
+
+def _size(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi + 1)))))))
+
+
+def draw(rng):
+    op = rng.choice(("quantize", "gemm", "adamw"))
+    if op == "quantize":
+        return dict(op=op, rows=_size(rng, 1, 16384), k=_size(rng, 1, 4096),
+                    type=rng.choice(("f32", "bf16", "f16")), fmt=rng.choice(("e4m3", "e5m2")),
+                    block_rows=rng.choice((1, 128)), want=rng.choice(("rows", "transposed", "both")))
+    if op == "gemm":
+        return dict(op=op, M=_size(rng, 1, 16384), N=_size(rng, 1, 14336),
+                    K=32 * _size(rng, 1, 128), a_fmt=rng.choice(("e4m3", "e5m2")),
+                    b_fmt=rng.choice(("e4m3", "e5m2")), a_block_rows=rng.choice((1, 1, 128)),
+                    b_block_rows=rng.choice((1, 128, 128)), out=rng.choice(("f32", "bf16", "f16")),
+                    alpha=rng.choice((1.0, 0.5)), accumulate=rng.choice((False, True)))
+    state = rng.choice(("f32", "fp8"))
+    count = rng.randint(1, 8)
+    return dict(op=op, sizes=",".join(str(_size(rng, 1, 20_000_000)) for _ in range(count)),
+                state=state, p_type=rng.choice(("f32", "f32", "bf16")),
+                g_type=rng.choice(("f32", "bf16", "f16")), step=_size(rng, 1, 100_000), lr=1e-4,
+                weight_decay=rng.choice((0.0, 0.1)))
+
+
+def _up(a, b):
+    return (a + b - 1) // b * b
+
+
+def _scale_shape(rows, k, block_rows):
+    """E8M0 bytes: one per block, K block index fastest, rows padded to 4 bytes."""
+    return (rows + block_rows - 1) // block_rows, 4 * ((k + 511) // 512)
+
+
+def work(case):
+    size = {"f32": 4, "bf16": 2, "f16": 2}
+    if case["op"] == "quantize":
+        r, k, b = case["rows"], case["k"], case["block_rows"]
+        n = r * k * size[case["type"]]
+        if case["want"] != "transposed":
+            n += r * _up(k, 32) + math.prod(_scale_shape(r, k, b))
+        if case["want"] != "rows":
+            n += k * _up(r, 32) + math.prod(_scale_shape(k, r, b))
+        return {"bytes": n, "flops": 0}
+    if case["op"] == "gemm":
+        M, N, K = case["M"], case["N"], case["K"]
+        n = (M + N) * K + M * N * size[case["out"]] * (2 if case["accumulate"] else 1)
+        n += math.prod(_scale_shape(M, K, case["a_block_rows"])) + math.prod(_scale_shape(N, K, case["b_block_rows"]))
+        return {"bytes": n, "flops": 2 * M * N * K}
+    n = sum(int(s) for s in case["sizes"].split(","))
+    state = 16 if case["state"] == "f32" else 4 + 4 / 128
+    return {"bytes": n * (2 * size[case["p_type"]] + size[case["g_type"]] + state), "flops": 0}
+
+
+# ----------------------------------------------------------------------------------------
+# Inputs
+# ----------------------------------------------------------------------------------------
+def _normal(gen, shape, std):
+    return torch.randn(shape, generator=gen, device=DEV) * std
+
+
+def _laplace(gen, shape, scale):
+    u = torch.rand(shape, generator=gen, device=DEV) - 0.5
+    return -scale * torch.sign(u) * torch.log1p(-2 * u.abs() * (1 - 2.0 ** -20))
+
+
+def _activations(gen, rows, k):
+    """N(0, 1) with one entry in a thousand a hundred times larger."""
+    x = _normal(gen, (rows, k), 1.0)
+    far = torch.rand((rows, k), generator=gen, device=DEV) < 0.001
+    return torch.where(far, x * 100, x)
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(seed)
+    if case["op"] == "quantize":
+        r, k = case["rows"], case["k"]
+        if case["type"] == "f32":
+            x = _normal(gen, (r, k), 0.02)
+        elif case["fmt"] == "e5m2":
+            x = _laplace(gen, (r, k), 1e-3)
+        else:
+            x = _activations(gen, r, k)
+        return dict(case, x=x.to(TYPES[case["type"]]))
+    if case["op"] == "gemm":
+        M, N, K = case["M"], case["N"], case["K"]
+        a = _laplace(gen, (M, K), 1e-3) if case["a_fmt"] == "e5m2" else _activations(gen, M, K)
+        a, sa = _quantize(a, case["a_fmt"], case["a_block_rows"])
+        b = _normal(gen, (N, K), 1.0 if case["b_block_rows"] == 1 else 0.02)
+        b, sb = _quantize(b, case["b_fmt"], case["b_block_rows"])
+        s = dict(case, a=a, sa=sa, b=b, sb=sb, d=None)
+        if case["accumulate"]:
+            s["d"] = _normal(gen, (M, N), 1e-2).to(TYPES[case["out"]])
+        return s
+    sizes = [int(n) for n in case["sizes"].split(",")]
+    params = [_normal(gen, (n,), 0.02).to(TYPES[case["p_type"]]) for n in sizes]
+    grads = [_laplace(gen, (n,), 1e-3).to(TYPES[case["g_type"]]) for n in sizes]
+    m = [_laplace(gen, (n,), 3e-4) for n in sizes]
+    v = [(_normal(gen, (n,), 1e-3).abs() + 1e-5) for n in sizes]
+    s = dict(case, params=params, grads=grads, seed=seed & 0xFFFFFFFF,
+             grad_scale=torch.rand((1,), generator=gen, device=DEV) + 0.5)
+    if case["state"] == "f32":
+        s["m"], s["v"] = m, [t * t for t in v]
+    else:
+        (s["m"], s["m_scales"]), (s["v"], s["v_scales"]) = (
+            zip(*[_quantize_flat(t) for t in ts]) for ts in (m, v))
+    return s
+
+
+# ----------------------------------------------------------------------------------------
+# Plain forms
+# ----------------------------------------------------------------------------------------
+#: The formats' largest finite value, as a fraction of the power of two above it.
+TOP = {"e4m3": (0.875, 9), "e5m2": (0.875, 16)}
+
+
+def _exponents(amax, fmt):
+    """The smallest e with F 2^e >= amax, in [-127, 127]; 0 where amax is 0."""
+    frac, above = TOP[fmt]
+    m, e = torch.frexp(amax)
+    e = e.to(torch.int32) - above + (m > frac).to(torch.int32)
+    return torch.where(amax == 0, 0, e.clamp(-127, 127))
+
+
+def _power(e):
+    """2^e in FP32, exactly, for e in [-126, 127]."""
+    return ((e + 127) << 23).view(torch.float32)
+
+
+def _quantize(x, fmt, block_rows):
+    """Codes (rows x k up to a multiple of 32, zeros past k) and E8M0 scales of x."""
+    rows, k = x.shape
+    R, Kb = (rows + block_rows - 1) // block_rows, (k + 127) // 128
+    xp = torch.nn.functional.pad(x.float(), (0, 128 * Kb - k, 0, R * block_rows - rows))
+    xb = xp.view(R, block_rows, Kb, 128)
+    e = _exponents(xb.abs().amax((1, 3)), fmt)
+    y = (xb * _power(-e)[:, None, :, None]).view(R * block_rows, Kb * 128)
+    codes = y[:rows, :_up(k, 32)].to(FP8[fmt]).view(torch.uint8).contiguous()
+    scales = torch.full(_scale_shape(rows, k, block_rows), 127, dtype=torch.uint8, device=x.device)
+    scales[:, :Kb] = (e + 127).to(torch.uint8)
+    return codes, scales
+
+
+def _dequantize(codes, scales, fmt, block_rows):
+    rows, K = codes.shape
+    s = scales.view(torch.float8_e8m0fnu).float()
+    s = s.repeat_interleave(block_rows, 0)[:rows].repeat_interleave(128, 1)[:, :K]
+    return codes.view(FP8[fmt]).float() * s
+
+
+def _quantize_flat(x):
+    """FP8 E4M3 codes of a vector, rounded to nearest, one E8M0 scale per 128 elements."""
+    n = x.numel()
+    xb = torch.nn.functional.pad(x, (0, _up(n, 128) - n)).view(-1, 128)
+    e = _exponents(xb.abs().amax(1), "e4m3")
+    codes = (xb * _power(-e)[:, None]).to(FP8["e4m3"]).view(torch.uint8).view(-1)[:n].contiguous()
+    return codes, (e + 127).to(torch.uint8)
+
+
+def _mix(h):
+    """The 32-bit finalizer of MurmurHash3, on int64 tensors or ints."""
+    h = h ^ (h >> 16)
+    h = (h * 0x85EBCA6B) & 0xFFFFFFFF
+    h = h ^ (h >> 13)
+    h = (h * 0xC2B2AE35) & 0xFFFFFFFF
+    return h ^ (h >> 16)
+
+
+def _shift(s, _):
+    """One step of Marsaglia's 32-bit xorshift generator (13, 17, 5)."""
+    s = s ^ ((s << 13) & 0xFFFFFFFF)
+    s = s ^ (s >> 17)
+    return s ^ ((s << 5) & 0xFFFFFFFF)
+
+
+def _noise(n, seed, step, tensor):
+    """32 random bits per element: a hash per 8 elements, then one xorshift step each."""
+    key = _mix(_mix(_mix(seed) ^ (step & 0xFFFFFFFF)) ^ tensor)
+    q = torch.arange((n + 7) // 8, device=DEV, dtype=torch.int64)
+    first = _mix((q * 0x9E3779B1 + key) & 0xFFFFFFFF) | 1
+    return torch.stack(list(itertools.accumulate([first] + 7 * [0], _shift)), 1).view(-1)[:n]
+
+
+def _round_fp8(x, bits, keep):
+    """E4M3 codes of a vector with one E8M0 scale per 128 elements; an element's distance
+    above the code below it, in steps and cut to 20 bits, is rounded up when its sum
+    with bits / 2^16 reaches 1.  keep: a nonzero element keeps a nonzero code."""
+    n = x.numel()
+    xb = torch.nn.functional.pad(x, (0, _up(n, 128) - n)).view(-1, 128)
+    e = _exponents(xb.abs().amax(1), "e4m3")
+    y = (xb * _power(-e)[:, None]).view(-1)[:n]
+    ex = ((y.view(torch.int32) >> 23) & 255).clamp(min=121) - 127
+    t = (y.abs() * _power(23 - ex)).to(torch.int64)
+    t = (t + (bits << 4)) >> 20
+    if keep:
+        t = torch.where((x > 0) & (t == 0), 1, t)
+    z = torch.copysign(t.float() * _power(ex - 3), y)
+    return z.to(FP8["e4m3"]).view(torch.uint8), (e + 127).to(torch.uint8)
+
+
+def _round_bf16(x, bits):
+    """FP32 to bf16: the 16 bits cut off carry when their sum with bits reaches 2^16."""
+    up = ((x.view(torch.int32).to(torch.int64) & 0xFFFFFFFF) + bits) & 0xFFFF0000
+    return torch.where(up >= 1 << 31, up - (1 << 32), up).to(torch.int32).view(torch.float32).to(torch.bfloat16)
+
+
+def _constants(s):
+    b1, b2, t = 0.9, 0.999, s["step"]
+    return (b1, 1 - b1, b2, 1 - b2, 1 - s["lr"] * s["weight_decay"], s["lr"] / (1 - b1 ** t),
+            1 / math.sqrt(1 - b2 ** t), 1e-8)
+
+
+def _adamw_plain(s, i):
+    b1, c1, b2, c2, decay, size, rbc, eps = (torch.tensor(c, dtype=torch.float32).item() for c in _constants(s))
+    p, fp8 = s["params"][i], s["state"] == "fp8"
+    n = p.numel()
+    g = s["grads"][i].float() * s["grad_scale"]
+    if fp8:
+        bits = _noise(n, s["seed"], s["step"], i)
+        m, r = (_dequantize_flat(s[x][i], s[x + "_scales"][i]) for x in ("m", "v"))
+        v = r * r
+    else:
+        m, v = s["m"][i], s["v"][i]
+    m = b1 * m + c1 * g
+    v = b2 * v + (c2 * g) * g
+    r = torch.sqrt(v)
+    new = p.float() * decay - (size * m) / (r * rbc + eps)
+    if p.dtype == torch.bfloat16:
+        new = _round_bf16(new, bits & 0xFFFF if fp8 else _noise(n, s["seed"], s["step"], i) & 0xFFFF)
+    p.copy_(new)
+    if not fp8:
+        s["m"][i].copy_(m)
+        s["v"][i].copy_(v)
+        return
+    for x, y, b, keep in (("m", m, bits & 0xFFFF, False), ("v", r, bits >> 16, True)):
+        codes, scales = _round_fp8(y, b, keep)
+        s[x][i].copy_(codes)
+        s[x + "_scales"][i].copy_(scales)
+
+
+def _dequantize_flat(codes, scales):
+    n = codes.numel()
+    f = scales.view(torch.float8_e8m0fnu).float().repeat_interleave(128)[:n]
+    return codes.view(FP8["e4m3"]).float() * f
+
+
+def _quantized(got, fmt):
+    """What a quantiser returns, as the values that its codes and scale bytes stand for."""
+    return [t.view(FP8[fmt] if i % 2 == 0 else torch.float8_e8m0fnu) for i, t in enumerate(got) if t is not None]
+
+
+def run(state):
+    s = state
+    if s["op"] == "quantize":
+        x, fmt, b, want = s["x"], s["fmt"], s["block_rows"], s["want"]
+        if own:
+            import block_scaled_precision_fp8_amd as bs
+            got = bs.fp8_quantize_block128(x, fmt, b, rows=want != "transposed", transposed=want != "rows")
+        else:
+            got = _quantize(x, fmt, b) if want != "transposed" else ()
+            got += _quantize(x.t(), fmt, b) if want != "rows" else ()
+        return _quantized(got, fmt)
+    if s["op"] == "gemm":
+        if own:
+            import block_scaled_precision_fp8_amd as bs
+            return bs.scaled_gemm_block128(s["a"], s["sa"], s["b"], s["sb"], s["a_fmt"], s["b_fmt"],
+                                           s["a_block_rows"], s["b_block_rows"], out=s["out"],
+                                           alpha=s["alpha"], c=s["d"],
+                                           beta=1.0 if s["accumulate"] else 0.0, d=s["d"])
+        a = _dequantize(s["a"], s["sa"], s["a_fmt"], s["a_block_rows"])
+        b = _dequantize(s["b"], s["sb"], s["b_fmt"], s["b_block_rows"])
+        d = s["alpha"] * (a @ b.t())
+        if s["accumulate"]:
+            return s["d"].copy_(d + s["d"].float())
+        return d.to(TYPES[s["out"]])
+    fp8 = s["state"] == "fp8"
+    if own:
+        import block_scaled_precision_fp8_amd as bs
+        bs.adamw_step(s["params"], s["grads"], s["m"], s["v"],
+                      s["m_scales"] if fp8 else None, s["v_scales"] if fp8 else None,
+                      lr=s["lr"], beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=s["weight_decay"],
+                      step=s["step"], grad_scale=s["grad_scale"], seed=s["seed"])
+    else:
+        [_adamw_plain(s, i) for i in range(len(s["params"]))]
+    out = {"p": list(s["params"])}
+    if not fp8:
+        return dict(out, m=list(s["m"]), v=list(s["v"]))
+    for x in ("m", "v"):
+        out[x] = [t.view(FP8["e4m3"]) for t in s[x]]
+        out[x + "_scales"] = [t.view(torch.float8_e8m0fnu) for t in s[x + "_scales"]]
+    return out
+
+
+# ----------------------------------------------------------------------------------------
+# The same from the definitions, in 64 bits
+# ----------------------------------------------------------------------------------------
+def _grid(fmt):
+    """The finite non-negative values of a format, by code."""
+    bias, man, top = (7, 3, 0x7E) if fmt == "e4m3" else (15, 2, 0x7B)
+    parts = [divmod(c, 2 ** man) for c in range(top + 1)]
+    return torch.tensor([math.ldexp(f + (2 ** man if e else 0), max(e, 1) - bias - man) for e, f in parts],
+                        dtype=torch.float64, device=DEV)
+
+
+def _two_to(e):
+    """2^e in 64 bits, from a table of the exact powers."""
+    return torch.tensor([math.ldexp(1.0, i) for i in range(-400, 401)], dtype=torch.float64, device=DEV)[e.long() + 400]
+
+
+def _exact_scale(amax, fmt):
+    """The smallest power of two that brings amax to at most the format's largest value."""
+    top = _grid(fmt)[-1]
+    s = _two_to(torch.ceil(torch.log2(amax / top)).clamp(-127, 127))
+    s = torch.where((s / 2 * top >= amax) & (s > 2.0 ** -127), s / 2, s)
+    s = torch.where(s * top < amax, s * 2, s)
+    return torch.where(amax == 0, 1.0, s)
+
+
+def _exact_nearest(y, grid):
+    """The grid value nearest to each |y|, ties to the even code, with y's sign."""
+    a = y.abs()
+    hi = torch.searchsorted(grid, a).clamp(max=grid.numel() - 1)
+    lo = (hi - 1).clamp(min=0)
+    below, above = a - grid[lo], grid[hi] - a
+    pick = torch.where((below < above) | ((below == above) & (lo % 2 == 0)), lo, hi)
+    return torch.copysign(grid[pick], y)
+
+
+def _exact_quantize(x, fmt, block_rows):
+    x = x.double()
+    rows, k = x.shape
+    ri = torch.arange(rows, device=DEV) // block_rows
+    amax = torch.stack([c.abs().amax(1) for c in x.split(128, 1)], 1)
+    amax = torch.zeros((int(ri[-1]) + 1, amax.shape[1]), dtype=torch.float64, device=DEV).index_reduce_(0, ri, amax, "amax")
+    s = _exact_scale(amax, fmt)
+    grid, ki = _grid(fmt), torch.arange(k, device=DEV) // 128
+    codes = torch.zeros((rows, _up(k, 32)), dtype=torch.float64, device=DEV)
+    for r in range(0, rows, 2048):
+        codes[r:r + 2048, :k] = _exact_nearest(x[r:r + 2048] / s[ri[r:r + 2048]][:, ki], grid)
+    scales = torch.ones(_scale_shape(rows, k, block_rows), dtype=torch.float64, device=DEV)
+    scales[:, :s.shape[1]] = s
+    return [codes, scales]
+
+
+def _signed(codes, fmt):
+    c = codes.long()
+    v = _grid(fmt)[c & 127]
+    return torch.where(c >= 128, -v, v)
+
+
+def _exact_operand(codes, scales, fmt, block_rows):
+    rows, K = codes.shape
+    v = _signed(codes, fmt)
+    ri, ki = torch.arange(rows, device=DEV) // block_rows, torch.arange(K, device=DEV) // 128
+    return v * _two_to(scales.long() - 127)[ri][:, ki]
+
+
+def _exact_adamw(s, i):
+    b1, c1, b2, c2, decay, size, rbc, eps = _constants(s)
+    p, fp8 = s["params"][i].double(), s["state"] == "fp8"
+    n = p.numel()
+    g = s["grads"][i].double() * s["grad_scale"].double()
+    at = torch.arange(n, device=DEV) // 128
+    if fp8:
+        m, r = (_signed(s[x][i], "e4m3") * _two_to(s[x + "_scales"][i].long() - 127)[at] for x in ("m", "v"))
+        v = r.square()
+    else:
+        m, v = s["m"][i].double(), s["v"][i].double()
+    m, v = m * b1 + g * c1, v * b2 + g.square() * c2
+    r = v.sqrt()
+    p = p * decay - size * m / (r * rbc + eps)
+    u = None
+    if fp8 or s["p_type"] == "bf16":
+        u = _noise(n, s["seed"], s["step"], i)
+    if s["p_type"] == "bf16":
+        f, e = torch.frexp(p)
+        t = torch.floor(f.abs() * 2 ** 24)
+        t = torch.floor((t + (u & 0xFFFF)) / 65536)
+        p = torch.copysign(t * _two_to(e - 8), p)
+    if not fp8:
+        return p, (m, None), (v, None)
+    out = []
+    for x, b in ((m, u & 0xFFFF), (r, u >> 16)):
+        amax = torch.zeros(int(at[-1]) + 1, dtype=torch.float64, device=DEV).index_reduce_(0, at, x.abs(), "amax")
+        scale = _exact_scale(amax, "e4m3")
+        y = x.abs() / scale[at]
+        step = _two_to(torch.frexp(y)[1].clamp(min=-5) - 4)
+        t = torch.floor((torch.floor(y / step * 2 ** 20) + b * 16) / 2 ** 20)
+        if x is r:
+            t = torch.where((x > 0) & (t == 0), torch.ones_like(t), t)
+        out.append((torch.copysign(t * step, x), scale))
+    return p, out[0], out[1]
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] == "quantize":
+        out = []
+        if case["want"] != "transposed":
+            out += _exact_quantize(s["x"], case["fmt"], case["block_rows"])
+        if case["want"] != "rows":
+            out += _exact_quantize(s["x"].t(), case["fmt"], case["block_rows"])
+        return out
+    if case["op"] == "gemm":
+        a = _exact_operand(s["a"], s["sa"], case["a_fmt"], case["a_block_rows"])
+        b = _exact_operand(s["b"], s["sb"], case["b_fmt"], case["b_block_rows"])
+        d = case["alpha"] * (a @ b.t().contiguous())
+        return d + s["d"].double() if case["accumulate"] else d
+    got = [_exact_adamw(s, i) for i in range(len(s["params"]))]
+    out = {"p": [p for p, _, _ in got], "m": [m for _, (m, _), _ in got], "v": [v for _, _, (v, _) in got]}
+    if case["state"] == "fp8":
+        out["m_scales"] = [e for _, (_, e), _ in got]
+        out["v_scales"] = [e for _, _, (_, e) in got]
+    return out
