@@ -101,8 +101,8 @@ def _up(a, b):
 
 
 def _scale_shape(rows, k, block_rows):
-    """E8M0 bytes: one per block, K block index fastest, rows padded to 4 bytes."""
-    return (rows + block_rows - 1) // block_rows, 4 * ((k + 511) // 512)
+    """E8M0 bytes [K / 512][rows of blocks][4]: byte (g, r, j) belongs to K block 4 g + j."""
+    return (k + 511) // 512, (rows + block_rows - 1) // block_rows, 4
 
 
 def work(case):
@@ -210,14 +210,14 @@ def _quantize(x, fmt, block_rows):
     e = _exponents(xb.abs().amax((1, 3)), fmt)
     y = (xb * _power(-e)[:, None, :, None]).view(R * block_rows, Kb * 128)
     codes = y[:rows, :_up(k, 32)].to(FP8[fmt]).view(torch.uint8).contiguous()
-    scales = torch.full(_scale_shape(rows, k, block_rows), 127, dtype=torch.uint8, device=x.device)
+    scales = torch.full((R, _up(Kb, 4)), 127, dtype=torch.uint8, device=x.device)
     scales[:, :Kb] = (e + 127).to(torch.uint8)
-    return codes, scales
+    return codes, scales.view(R, -1, 4).transpose(0, 1).contiguous()
 
 
 def _dequantize(codes, scales, fmt, block_rows):
     rows, K = codes.shape
-    s = scales.view(torch.float8_e8m0fnu).float()
+    s = scales.transpose(0, 1).reshape(scales.shape[1], -1).view(torch.float8_e8m0fnu).float()
     s = s.repeat_interleave(block_rows, 0)[:rows].repeat_interleave(128, 1)[:, :K]
     return codes.view(FP8[fmt]).float() * s
 
@@ -411,9 +411,10 @@ def _exact_quantize(x, fmt, block_rows):
     codes = torch.zeros((rows, _up(k, 32)), dtype=torch.float64, device=DEV)
     for r in range(0, rows, 2048):
         codes[r:r + 2048, :k] = _exact_nearest(x[r:r + 2048] / s[ri[r:r + 2048]][:, ki], grid)
-    scales = torch.ones(_scale_shape(rows, k, block_rows), dtype=torch.float64, device=DEV)
-    scales[:, :s.shape[1]] = s
-    return [codes, scales]
+    groups, R, four = _scale_shape(rows, k, block_rows)
+    scales = torch.ones((groups * four, R), dtype=torch.float64, device=DEV)
+    scales[:s.shape[1]] = s.t()
+    return [codes, scales.view(groups, four, R).transpose(1, 2)]
 
 
 def _signed(codes, fmt):
@@ -426,7 +427,7 @@ def _exact_operand(codes, scales, fmt, block_rows):
     rows, K = codes.shape
     v = _signed(codes, fmt)
     ri, ki = torch.arange(rows, device=DEV) // block_rows, torch.arange(K, device=DEV) // 128
-    return v * _two_to(scales.long() - 127)[ri][:, ki]
+    return v * _two_to(scales.long() - 127)[ki // 4, :, ki % 4].t()[ri]
 
 
 def _exact_adamw(s, i):
