@@ -20,9 +20,16 @@ Functions (same names as the C ABI):
   scaled_gemm_mx(a, a_scales, b, b_scales, block, scale, out="bf16", ...) -> d
   scaled_gemm_quantize_a(x, b, b_scales, ...) -> d (A quantised inside the GEMM;
                  optionally also its codes and scales)
+  fp8_quantize_block128(x, fmt="e4m3", block_rows=1|128, rows=True, transposed=False)
+                 -> (codes, scales), those of x^T, or both
+  scaled_gemm_block128(a, a_scales, b, b_scales, a_fmt, b_fmt, a_block_rows=1,
+                 b_block_rows=128, out="bf16", ...) -> d
+  adamw_step(params, grads, m, v, m_scales=None, v_scales=None, lr=..., ...) (in place)
+  adamw_states(params, state="f32"|"fp8") -> zeroed (m, v, m_scales, v_scales)
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -80,6 +87,13 @@ def lib() -> ctypes.CDLL:
     L.scaled_gemm_mx.argtypes = [i64, i64, i64, c_int, c_int, vp, vp, vp, vp, ctypes.c_float, vp, i64,
                                  ctypes.c_float, c_int, vp, i64, vp]
     L.scaled_gemm_mx.restype = c_int
+    L.fp8_quantize_block128.argtypes = [vp, c_int, i64, i64, i64, c_int, c_int, vp, vp, vp, vp, vp]
+    L.fp8_quantize_block128.restype = c_int
+    L.scaled_gemm_block128.argtypes = [i64, i64, i64, c_int, vp, vp, c_int, c_int, vp, vp, c_int,
+                                       ctypes.c_float, vp, i64, ctypes.c_float, c_int, vp, i64, vp]
+    L.scaled_gemm_block128.restype = c_int
+    L.adamw_step.argtypes = [vp, i64, c_int, c_int, c_int, vp, vp]
+    L.adamw_step.restype = c_int
     L.bsfp8_status_string.argtypes = [c_int]
     L.bsfp8_status_string.restype = ctypes.c_char_p
     L.bsfp8_version.argtypes = []
@@ -511,3 +525,211 @@ def scaled_gemm_mx(a, a_scales, b, b_scales, block: int = 32, scale: str = "e8m0
                               OUTS[out], _dev_ptr(d), _ld(d, M, N), _stream(a))
     _check(st, "scaled_gemm_mx")
     return d
+
+
+# ---------------------------------------------------------------------------
+# Blocks of 128 and the optimizer step
+# ---------------------------------------------------------------------------
+def _call(device, fn, *args) -> int:
+    """fn(*args) with `device` current (a launch goes to the current device)."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
+def block128_scale_shape(rows: int, k: int, block_rows: int) -> Tuple[int, int, int]:
+    """Shape of the E8M0 scale bytes of a rows x k operand: [ceil(k / 512)][scale rows][4]."""
+    return (k + 511) // 512, (rows + block_rows - 1) // block_rows, 4
+
+
+def _block_rows(value, name: str = "block_rows") -> int:
+    if value not in (1, 128):
+        raise ValueError(f"unknown {name} {value!r}; expected 1 or 128")
+    return value
+
+
+def _element_type(t, name: str) -> int:
+    import torch
+    types = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    _tensor(t, name, tuple(types))
+    return types[t.dtype]
+
+
+def fp8_quantize_block128(x, fmt: str = "e4m3", block_rows: int = 1, rows: bool = True,
+                          transposed: bool = False, codes=None, scales=None, codes_t=None,
+                          scales_t=None):
+    """Quantise a rows x k CUDA tensor (float32, bfloat16 or float16, unit column stride)
+    to FP8 codes with one E8M0 scale per 1 x 128 or 128 x 128 block.  Returns (codes,
+    scales) of x (rows=True), of x^T (transposed=True), or all four, from one read of x.
+    Codes are rows x kp, kp = k rounded up to a multiple of 32 (zeros past k); scales as
+    block128_scale_shape says, bytes e + 127."""
+    import torch
+    xt = _element_type(x, "x")
+    if x.dim() != 2 or (x.numel() > 0 and x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be 2-D with unit column stride")
+    n, k = x.shape
+    if n > 1 and x.stride(0) < k:
+        raise ValueError(f"x rows overlap (row stride {x.stride(0)} < {k})")
+    f = _fp8_fmt(fmt)
+    _block_rows(block_rows)
+    if not rows and not transposed:
+        raise ValueError("rows or transposed must be set")
+    dev = x.device
+
+    def outs(want, r, w, c, s, suffix):
+        if not want:
+            if c is not None or s is not None:
+                raise ValueError(f"codes{suffix} and scales{suffix} are for an orientation that is not asked for")
+            return ()
+        shape, sshape = (r, (w + 31) // 32 * 32), block128_scale_shape(r, w, block_rows)
+        if c is None:
+            c = torch.empty(shape, dtype=torch.uint8, device=dev)
+        else:
+            _packed(c, "codes" + suffix, shape, (torch.uint8,), dev)
+        if s is None:
+            s = torch.empty(sshape, dtype=torch.uint8, device=dev)
+        else:
+            _packed(s, "scales" + suffix, sshape, (torch.uint8,), dev)
+        return c, s
+
+    got = outs(rows, n, k, codes, scales, ""), outs(transposed, k, n, codes_t, scales_t, "_t")
+    if n and k:
+        p = [t.data_ptr() for t in got[0]] or [0, 0]
+        q = [t.data_ptr() for t in got[1]] or [0, 0]
+        st = _call(dev, lib().fp8_quantize_block128, x.data_ptr(), xt, n, k, _ld(x, n, k), block_rows, f,
+                   *p, *q, _stream(x))
+        _check(st, "fp8_quantize_block128")
+    return got[0] + got[1]
+
+
+def scaled_gemm_block128(a, a_scales, b, b_scales, a_fmt: str = "e4m3", b_fmt: str = "e4m3",
+                         a_block_rows: int = 1, b_block_rows: int = 128, out: str = "bf16",
+                         alpha: float = 1.0, c=None, beta: float = 0.0, d=None):
+    """D = alpha deq(A) deq(B) + beta C for operands of fp8_quantize_block128: a M x K codes,
+    b N x K codes (a K x N column-major operand), each with its E8M0 scales per 1 x 128
+    (block_rows 1) or 128 x 128 block.  c may be d itself, to accumulate in place."""
+    import torch
+    fa, fb = _fp8_fmt(a_fmt), _fp8_fmt(b_fmt)
+    _block_rows(a_block_rows, "a_block_rows")
+    _block_rows(b_block_rows, "b_block_rows")
+    u8 = (torch.uint8,)
+    _tensor(a, "a", u8)
+    dev = a.device
+    _tensor(b, "b", u8, dev)
+    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
+        raise ValueError(f"a ({tuple(a.shape)}) and b ({tuple(b.shape)}) must be 2-D with the same K")
+    (M, K), N = a.shape, b.shape[0]
+    if not a.is_contiguous() or not b.is_contiguous():
+        raise ValueError("a and b must be contiguous")
+    _packed(a_scales, "a_scales", block128_scale_shape(M, K, a_block_rows), u8, dev)
+    _packed(b_scales, "b_scales", block128_scale_shape(N, K, b_block_rows), u8, dev)
+    d, cp, ldc = _epilogue_tensors(d, c, beta, M, N, out, dev)
+    if M and N:
+        st = _call(dev, lib().scaled_gemm_block128, M, N, K, fa, a.data_ptr(), a_scales.data_ptr(),
+                   a_block_rows, fb, b.data_ptr(), b_scales.data_ptr(), b_block_rows, alpha, cp, ldc, beta,
+                   OUTS[out], d.data_ptr(), _ld(d, M, N), _stream(a))
+        _check(st, "scaled_gemm_block128")
+    return d
+
+
+class _AdamWArgs(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
+                ("seed", ctypes.c_uint32), ("lr_dev", ctypes.c_void_p), ("step_dev", ctypes.c_void_p),
+                ("grad_scale", ctypes.c_void_p), ("found_inf", ctypes.c_void_p)]
+
+
+def adamw_states(params, state: str = "f32"):
+    """Zeroed states of adamw_step: (m, v, m_scales, v_scales), lists of one tensor per
+    parameter.  "f32": FP32 moments, no scales (None).  "fp8": uint8 E4M3 codes of the first
+    moment and of the second moment's square root, and E8M0 scales per 128 elements."""
+    import torch
+    if state not in ("f32", "fp8"):
+        raise ValueError(f"unknown state {state!r}; expected 'f32' or 'fp8'")
+    dt = torch.float32 if state == "f32" else torch.uint8
+
+    def zeros():
+        return [torch.zeros(p.shape, dtype=dt, device=p.device) for p in params]
+
+    def scales():
+        if state == "f32":
+            return None
+        return [torch.zeros((p.numel() + 127) // 128, dtype=torch.uint8, device=p.device) for p in params]
+
+    return zeros(), zeros(), scales(), scales()
+
+
+def _scalar_ptr(t, name: str, dtype, device) -> int:
+    _tensor(t, name, (dtype,), device)
+    if t.numel() != 1:
+        raise ValueError(f"{name} must hold one element, got {t.numel()}")
+    return t.data_ptr()
+
+
+def adamw_step(params, grads, m, v, m_scales=None, v_scales=None, *, lr=1e-3, beta1: float = 0.9,
+               beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 1e-2, step=1,
+               grad_scale=None, found_inf=None, seed: int = 0) -> None:
+    """One AdamW step over lists of tensors, in place.
+
+    params: contiguous float32 or bfloat16 tensors of one dtype; grads: float32, bfloat16 or
+    float16, of the same sizes.  m, v: float32 moments, or (with m_scales and v_scales, see
+    adamw_states) uint8 E4M3 codes of m and sqrt(v), rounded stochastically.  bfloat16
+    parameters are rounded stochastically too; the random bits depend on (seed, step,
+    position in the list, element).
+
+    lr (float or one-element float32 tensor) and step (int >= 1 or one-element int64 tensor):
+    tensors are read on the device when the step runs, so a captured step follows them.
+    grad_scale: one-element float32 tensor that multiplies the gradients.  found_inf:
+    one-element float32 tensor; when it is not zero the step changes nothing."""
+    import torch
+    lists = [list(params), list(grads), list(m), list(v)]
+    fp8 = m_scales is not None or v_scales is not None
+    if fp8:
+        if m_scales is None or v_scales is None:
+            raise ValueError("m_scales and v_scales go together")
+        lists += [list(m_scales), list(v_scales)]
+    count = len(lists[0])
+    if any(len(x) != count for x in lists):
+        raise ValueError("params, grads, m, v and the scales must be lists of one length")
+    if count == 0:
+        return
+    p0, g0 = lists[0][0], lists[1][0]
+    _tensor(p0, "params[0]", (torch.float32, torch.bfloat16))
+    _tensor(g0, "grads[0]", (torch.float32, torch.bfloat16, torch.float16))
+    dev = p0.device
+    state_dt = torch.uint8 if fp8 else torch.float32
+    names = ("params", "grads", "m", "v", "m_scales", "v_scales")
+    dtypes = (p0.dtype, g0.dtype, state_dt, state_dt, torch.uint8, torch.uint8)
+    flat = array.array("q")
+    for i, row in enumerate(zip(*lists)):
+        n = row[0].numel() if isinstance(row[0], torch.Tensor) else 0
+        for j, t in enumerate(row):
+            if not isinstance(t, torch.Tensor) or t.dtype is not dtypes[j] or t.device != dev:
+                _tensor(t, f"{names[j]}[{i}]", (dtypes[j],), dev)
+            if t.numel() != (n if j < 4 else (n + 127) // 128) or not t.is_contiguous():
+                raise ValueError(f"{names[j]}[{i}] must be contiguous with "
+                                 f"{n if j < 4 else (n + 127) // 128} elements, got {tuple(t.shape)} "
+                                 f"(contiguous: {t.is_contiguous()})")
+            flat.append(t.data_ptr())
+        if not fp8:
+            flat.extend((0, 0))
+        flat.append(n)
+    args = _AdamWArgs(0.0, beta1, beta2, eps, weight_decay, 1, seed & 0xFFFFFFFF)
+    if isinstance(lr, torch.Tensor):
+        args.lr_dev = _scalar_ptr(lr, "lr", torch.float32, dev)
+    else:
+        args.lr = lr
+    if isinstance(step, torch.Tensor):
+        args.step_dev = _scalar_ptr(step, "step", torch.int64, dev)
+    else:
+        args.step = step
+    if grad_scale is not None:
+        args.grad_scale = _scalar_ptr(grad_scale, "grad_scale", torch.float32, dev)
+    if found_inf is not None:
+        args.found_inf = _scalar_ptr(found_inf, "found_inf", torch.float32, dev)
+    types = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    st = _call(dev, lib().adamw_step, flat.buffer_info()[0], count, types[p0.dtype], types[g0.dtype],
+               1 if fp8 else 0, ctypes.addressof(args), _stream(p0))
+    _check(st, "adamw_step")

@@ -3,12 +3,17 @@
 // nothing was launched.  No allocation, no synchronisation, no global state.
 #include "internal.h"
 
+#include <algorithm>
+#include <cmath>
 #include <limits>
+#include <new>
+#include <vector>
 
 namespace {
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline bool is_fp8(int f) { return f == BSFP8_E4M3 || f == BSFP8_E5M2; }
+inline bool is_element(int t) { return t == BSFP8_OUT_F32 || t == BSFP8_OUT_BF16 || t == BSFP8_OUT_F16; }
 constexpr int64_t kI32Max = std::numeric_limits<int32_t>::max();
 // scaled_gemm_quantize_a: from this many 128-wide output column tiles on, a
 // call that also asks for A's codes quantises A once and runs the per-tile
@@ -276,6 +281,107 @@ bsfp8_status scaled_gemm_quantize_a(int64_t M, int64_t N, int64_t K, const float
                                                     ep, stream));
 }
 
+bsfp8_status fp8_quantize_block128(const void* x, bsfp8_out x_type, int64_t rows, int64_t k, int64_t ld,
+                                   int block_rows, bsfp8_format fmt, uint8_t* codes, uint8_t* scales,
+                                   uint8_t* codes_t, uint8_t* scales_t, hipStream_t stream) {
+    if (!is_fp8(fmt) || !is_element(x_type) || (block_rows != 1 && block_rows != 128)) return BSFP8_ERR_UNSUPPORTED;
+    if (rows < 0 || k < 0 || ld < k || rows > kI32Max || k > kI32Max) return BSFP8_ERR_INVALID_ARG;
+    if ((codes == nullptr) != (scales == nullptr) || (codes_t == nullptr) != (scales_t == nullptr))
+        return BSFP8_ERR_INVALID_ARG;
+    if (rows == 0 || k == 0) return BSFP8_OK;
+    if (!x || (!codes && !codes_t)) return BSFP8_ERR_INVALID_ARG;
+    if (!aligned(x, x_type == BSFP8_OUT_F32 ? 4 : 2) || !aligned(codes, 16) || !aligned(codes_t, 16) ||
+        !aligned(scales, 4) || !aligned(scales_t, 4))
+        return BSFP8_ERR_INVALID_ARG;
+    if (((rows + 127) / 128) * ((k + 127) / 128) > kI32Max) return BSFP8_ERR_INVALID_ARG;
+    return from_hip(bsfp8::launch_quantize_block128(x, x_type, rows, k, ld, block_rows, fmt, codes, scales, codes_t,
+                                                    scales_t, stream));
+}
+
+bsfp8_status scaled_gemm_block128(int64_t M, int64_t N, int64_t K, bsfp8_format a_fmt, const void* a,
+                                  const void* a_scales, int a_block_rows, bsfp8_format b_fmt, const void* b,
+                                  const void* b_scales, int b_block_rows, float alpha, const void* c,
+                                  int64_t ldc, float beta, bsfp8_out out, void* d, int64_t ldd,
+                                  hipStream_t stream) {
+    if (!is_fp8(a_fmt) || !is_fp8(b_fmt) || !is_element(out)) return BSFP8_ERR_UNSUPPORTED;
+    if ((a_block_rows != 1 && a_block_rows != 128) || (b_block_rows != 1 && b_block_rows != 128))
+        return BSFP8_ERR_UNSUPPORTED;
+    if (M < 0 || N < 0 || K < 0 || (K % 32) != 0) return BSFP8_ERR_INVALID_ARG;
+    if (M > kI32Max || N > kI32Max || K > kI32Max) return BSFP8_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return BSFP8_OK;
+    const uintptr_t es = out == BSFP8_OUT_F32 ? 4 : 2;
+    if (!d || ldd < N || !aligned(d, es)) return BSFP8_ERR_INVALID_ARG;
+    if (beta != 0.0f && (!c || ldc < N || !aligned(c, es))) return BSFP8_ERR_INVALID_ARG;
+    const bsfp8::Epilogue ep{alpha, beta, beta != 0.0f ? c : nullptr, beta != 0.0f ? ldc : 0};
+    if (K == 0) return from_hip(bsfp8::launch_fill(M, N, out, d, ldd, ep, stream));
+    if (!a || !b || !a_scales || !b_scales) return BSFP8_ERR_INVALID_ARG;
+    if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_scales, 4) || !aligned(b_scales, 4))
+        return BSFP8_ERR_INVALID_ARG;
+    // the kernels address a 256-row band of an operand with 32-bit offsets
+    if (K >= (int64_t(1) << 23)) return BSFP8_ERR_UNSUPPORTED;
+    // the narrow form's grid: a workgroup per 32 x 32 tile
+    if (((M + 31) / 32) * (((N + 31) / 32 + 7) / 8 * 8) > kI32Max) return BSFP8_ERR_INVALID_ARG;
+    return from_hip(bsfp8::launch_gemm_block128(M, N, K, a_fmt, static_cast<const uint8_t*>(a),
+                                                static_cast<const uint8_t*>(a_scales), a_block_rows, b_fmt,
+                                                static_cast<const uint8_t*>(b),
+                                                static_cast<const uint8_t*>(b_scales), b_block_rows, out, d, ldd,
+                                                ep, stream));
+}
+
+bsfp8_status adamw_step(const bsfp8_adamw_tensor* tensors, int64_t count, bsfp8_out p_type, bsfp8_out g_type,
+                        bsfp8_state state, const bsfp8_adamw_args* args, hipStream_t stream) {
+    if (state != BSFP8_STATE_F32 && state != BSFP8_STATE_FP8) return BSFP8_ERR_UNSUPPORTED;
+    if ((p_type != BSFP8_OUT_F32 && p_type != BSFP8_OUT_BF16) || !is_element(g_type)) return BSFP8_ERR_UNSUPPORTED;
+    if (count < 0 || count > kI32Max || !args || (count > 0 && !tensors)) return BSFP8_ERR_INVALID_ARG;
+    const bool finite = std::isfinite(args->lr) && std::isfinite(args->eps) && std::isfinite(args->weight_decay);
+    if (!finite || args->eps < 0.0 || !(args->beta1 >= 0.0 && args->beta1 < 1.0) ||
+        !(args->beta2 >= 0.0 && args->beta2 < 1.0))
+        return BSFP8_ERR_INVALID_ARG;
+    if (!args->step_dev && args->step < 1) return BSFP8_ERR_INVALID_ARG;
+    if (!aligned(args->lr_dev, 4) || !aligned(args->step_dev, 8) || !aligned(args->grad_scale, 4) ||
+        !aligned(args->found_inf, 4))
+        return BSFP8_ERR_INVALID_ARG;
+    const bool fp8 = state == BSFP8_STATE_FP8;
+    const int64_t ps = p_type == BSFP8_OUT_F32 ? 4 : 2, gs = g_type == BSFP8_OUT_F32 ? 4 : 2, ss = fp8 ? 1 : 4;
+    // byte ranges that are written, and those that are only read (the gradients)
+    struct Range { uintptr_t at, end; bool written; };
+    std::vector<Range> ranges;
+    try {
+        ranges.reserve(static_cast<size_t>(count) * 6);
+        for (int64_t i = 0; i < count; ++i) {
+            const bsfp8_adamw_tensor& t = tensors[i];
+            if (t.n < 0 || t.n > (int64_t(1) << 40)) return BSFP8_ERR_INVALID_ARG;
+            if (t.n == 0) continue;
+            if (!t.p || !t.g || !t.m || !t.v || (fp8 && (!t.m_scales || !t.v_scales))) return BSFP8_ERR_INVALID_ARG;
+            if (!aligned(t.p, ps) || !aligned(t.g, gs) || !aligned(t.m, ss) || !aligned(t.v, ss))
+                return BSFP8_ERR_INVALID_ARG;
+            auto add = [&](const void* p, int64_t bytes, bool w) {
+                const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+                ranges.push_back({a, a + static_cast<uintptr_t>(bytes), w});
+            };
+            add(t.p, t.n * ps, true);
+            add(t.g, t.n * gs, false);
+            add(t.m, t.n * ss, true);
+            add(t.v, t.n * ss, true);
+            if (fp8) {
+                add(t.m_scales, (t.n + 127) / 128, true);
+                add(t.v_scales, (t.n + 127) / 128, true);
+            }
+        }
+        std::sort(ranges.begin(), ranges.end(), [](const Range& x, const Range& y) { return x.at < y.at; });
+    } catch (const std::bad_alloc&) {
+        return BSFP8_ERR_INVALID_ARG;
+    }
+    // the furthest ends so far of written and of read ranges
+    uintptr_t wend = 0, rend = 0;
+    for (const Range& r : ranges) {
+        if (r.at < wend || (r.written && r.at < rend)) return BSFP8_ERR_INVALID_ARG;
+        (r.written ? wend : rend) = std::max(r.written ? wend : rend, r.end);
+    }
+    if (ranges.empty()) return BSFP8_OK;
+    return from_hip(bsfp8::launch_adamw(tensors, count, p_type, g_type, state, *args, stream));
+}
+
 bsfp8_status scaled_gemm_ex(int64_t M, int64_t N, int64_t K, bsfp8_format a_fmt, const void* a,
                             const void* a_scales, bsfp8_format b_fmt, const void* b,
                             const void* b_scales, float alpha, const void* c, int64_t ldc,
@@ -305,6 +411,6 @@ const char* bsfp8_status_string(bsfp8_status s) {
     }
 }
 
-int bsfp8_version(void) { return (0 << 16) | 5; }
+int bsfp8_version(void) { return (0 << 16) | 6; }
 
 }  // extern "C"

@@ -28,6 +28,12 @@ hipError_t launch_mxfp4_quantize(const float* x, int64_t rows, int64_t k, int64_
 // E2M1 with blocks of `block` (32, 16, 8) K elements and sfmt block scales
 hipError_t launch_mx_quantize(const float* x, int64_t rows, int64_t k, int64_t ld, int block,
                               int sfmt, uint8_t* packed, void* scales, hipStream_t stream);
+// FP8 with one E8M0 scale per 1 x 128 or 128 x 128 block (block_rows 1 or 128)
+// of x (x_type: its element type); codes / codes_t null: that orientation is
+// not wanted.
+hipError_t launch_quantize_block128(const void* x, int x_type, int64_t rows, int64_t k, int64_t ld, int block_rows,
+                                    int fmt, uint8_t* codes, uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t,
+                                    hipStream_t stream);
 // The GEMM epilogue: D = alpha * (A B) + beta * C, C of D's element type.
 // beta == 0 means C is not read (c may be null).  row_scale (col_scale), when
 // set, multiplies output row m (column n) by row_scale[m] (col_scale[n]): the
@@ -103,6 +109,14 @@ hipError_t launch_gemm_mx_fp4(int64_t M, int64_t N, int64_t K, int block, const 
 hipError_t launch_gemm_mx(int64_t M, int64_t N, int64_t K, int block, int sfmt, const uint8_t* a,
                           const void* a_scales, const uint8_t* b, const void* b_scales, int out,
                           void* d, int64_t ldd, const Epilogue& ep, hipStream_t stream);
+// FP8 operands with one E8M0 scale per 1 x 128 or 128 x 128 block.
+hipError_t launch_gemm_block128(int64_t M, int64_t N, int64_t K, int a_fmt, const uint8_t* a, const uint8_t* a_scales,
+                                int a_block_rows, int b_fmt, const uint8_t* b, const uint8_t* b_scales,
+                                int b_block_rows, int out, void* d, int64_t ldd, const Epilogue& ep,
+                                hipStream_t stream);
+// One AdamW step over count tensors (checked by the API layer).
+hipError_t launch_adamw(const bsfp8_adamw_tensor* tensors, int64_t count, int p_type, int g_type, int state,
+                        const bsfp8_adamw_args& args, hipStream_t stream);
 // K = 0: D = beta * C (zeros when beta == 0).
 hipError_t launch_fill(int64_t M, int64_t N, int out, void* d, int64_t ldd, const Epilogue& ep,
                        hipStream_t stream);

@@ -350,6 +350,132 @@ bsfp8_status scaled_gemm_quantize_a(int64_t M, int64_t N, int64_t K, const float
                                     hipStream_t stream);
 
 /*
+ * Blocks of 128: FP8 codes with one power-of-two scale (an E8M0 byte, as for
+ * MXFP4) per 1 x 128 block of a row, or per 128 x 128 block.  Activations and
+ * gradients usually take 1 x 128 blocks, weights 128 x 128 blocks, whose
+ * transpose has the same scales.
+ *
+ * Code matrices are rows x kp bytes with row stride kp = k rounded up to a
+ * multiple of 32; columns k .. kp-1 hold zero codes, so any k is accepted and
+ * kp is the K of the GEMM.  Scale bytes lie in words of four K blocks,
+ * [ceil(k / 512)][R][4] with R = rows (1 x 128) or ceil(rows / 128)
+ * (128 x 128): byte (g, r, j) is the scale of K block 4 g + j of scale row r.
+ * The words are 4-byte aligned.
+ */
+
+/*
+ * fp8_quantize_block128 -- block-of-128 FP8 quantisation of x, of its
+ * transpose, or of both from one read.
+ *
+ * x:      rows x k elements of type x_type (BSFP8_OUT_F32, BSFP8_OUT_BF16 or
+ *         BSFP8_OUT_F16), row-major, leading dimension ld >= k, aligned to its
+ *         element size.  16-byte aligned x with a row stride of a multiple of
+ *         16 bytes is read with 16-byte loads; anything else element by element.
+ * rows, k: >= 0, any value, at most 2^31 - 1.
+ * block_rows: 1 (1 x 128 blocks) or 128 (128 x 128 blocks); for the transpose
+ *         the blocks are those of x^T.
+ * codes, scales:     out, the codes and scales of x; both NULL: not wanted.
+ * codes_t, scales_t: out, those of x^T (k rows, K = rows); both NULL: not wanted.
+ *         Code buffers are 16-byte aligned.  At least one pair must be given.
+ *
+ * Per block: e = the smallest integer with F * 2^e >= max |x| (0 when that is
+ * 0), clamped to [-127, 127]; scale byte e + 127; code = round-to-nearest-even
+ * of x * 2^-e (exact scaling).  A block with an infinity or a NaN gets the
+ * scale byte 255 (NaN) and NaN codes (0x7F).  Unused bytes of the last scale
+ * word are 127.  Bit-exact.  rows == 0 or k == 0 writes nothing.
+ */
+bsfp8_status fp8_quantize_block128(const void* x, bsfp8_out x_type, int64_t rows, int64_t k, int64_t ld,
+                                   int block_rows, bsfp8_format fmt, uint8_t* codes, uint8_t* scales,
+                                   uint8_t* codes_t, uint8_t* scales_t, hipStream_t stream);
+
+/*
+ * scaled_gemm_block128 -- D = alpha * deq(A) deq(B) + beta * C for operands
+ * written by fp8_quantize_block128.
+ *
+ * a: M x K codes, a_scales E8M0 words [ceil(K / 512)][M or ceil(M / 128)][4]
+ * for a_block_rows 1 or 128; b: N x K codes (the K x N column-major operand)
+ * likewise.  a and b 16-byte aligned, the scales 4-byte aligned.  All formats
+ * (E4M3, E5M2) and block shapes mix.  K a multiple of 32, below 2^23 (the
+ * kernels address a 256-row band of an operand with 32-bit offsets; larger K
+ * returns BSFP8_ERR_UNSUPPORTED).  alpha, c, ldc, beta, out, d, ldd: as for
+ * scaled_gemm_ex.  A NaN scale makes every output that uses its block NaN.
+ *
+ * 16-bit outputs run on the block-scaled FP8 matrix instruction, which takes
+ * the E8M0 bytes itself; FP32 output widens the codes, times their scale, to
+ * bf16 (exact down to 2^-126) and uses the bf16 instruction.  Accuracy as for
+ * scaled_gemm_ex.
+ */
+bsfp8_status scaled_gemm_block128(int64_t M, int64_t N, int64_t K, bsfp8_format a_fmt, const void* a,
+                                  const void* a_scales, int a_block_rows, bsfp8_format b_fmt, const void* b,
+                                  const void* b_scales, int b_block_rows, float alpha, const void* c,
+                                  int64_t ldc, float beta, bsfp8_out out, void* d, int64_t ldd,
+                                  hipStream_t stream);
+
+/*
+ * The states of an AdamW step: FP32, or FP8 (E4M3 codes with one E8M0 scale
+ * per 128 consecutive elements).
+ */
+typedef enum {
+    BSFP8_STATE_F32 = 0,
+    BSFP8_STATE_FP8 = 1
+} bsfp8_state;
+
+/* One tensor of an AdamW step: n contiguous elements, every pointer a device
+ * pointer aligned to its element size. */
+typedef struct {
+    void* p;             /* parameters, in and out */
+    const void* g;       /* gradients */
+    void* m;             /* first moment, in and out: FP32 values, or E4M3 codes */
+    void* v;             /* FP32: the second moment; FP8: E4M3 codes of its square root */
+    uint8_t* m_scales;   /* FP8: E8M0 [ceil(n / 128)], in and out; FP32: NULL */
+    uint8_t* v_scales;
+    int64_t n;           /* >= 0 */
+} bsfp8_adamw_tensor;
+
+/* What the tensors of a step share.  Pointers are device pointers, read when
+ * the kernel runs, so that a captured step follows them; NULL: not used. */
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;               /* the number of this step, >= 1 */
+    uint32_t seed;              /* of the stochastic rounding */
+    const float* lr_dev;        /* replaces lr */
+    const int64_t* step_dev;    /* replaces step */
+    const float* grad_scale;    /* multiplies every gradient */
+    const float* found_inf;     /* not zero: the step changes nothing */
+} bsfp8_adamw_args;
+
+/*
+ * adamw_step -- one step of AdamW (decoupled weight decay) over `count`
+ * tensors in one launch per 48 tensors.  `tensors` and `args` are host arrays,
+ * read during the call.
+ *
+ * Per element, in FP32 with each operation rounded once (the constants in
+ * parentheses are formed in 64 bits and rounded to FP32):
+ *   g  = gradient * grad_scale
+ *   m' = (beta1) m + (1 - beta1) g          v' = (beta2) v + ((1 - beta2) g) g
+ *   p' = (1 - lr weight_decay) p - ((lr / (1 - beta1^t)) m') / ((1 / sqrt(1 - beta2^t)) sqrt(v') + (eps))
+ *
+ * p_type:  FP32 or bf16 parameters; g_type: FP32, bf16 or FP16 gradients.
+ * state:   FP32 keeps m' and v'.  FP8 keeps E4M3 codes of m' and of
+ *          r' = sqrt(v') (v = r * r when read back), scaled per 128 elements
+ *          as fp8_quantize_block128 does and rounded stochastically: with y the
+ *          scaled magnitude cut to 2^-20 of its code step, the code above is
+ *          taken when y's distance from the code below, in steps, plus b / 2^16
+ *          reaches 1.  A nonzero r' keeps a nonzero code.  bf16 parameters are
+ *          rounded likewise: the 16 bits cut off carry when their sum with b
+ *          reaches 2^16.  The random bits b depend on (seed, step, position of
+ *          the tensor in `tensors`, element) only, so a step is reproducible.
+ * Zeroed codes and scale bytes are valid initial states, as zeroed FP32 ones.
+ *
+ * beta1, beta2 in [0, 1); eps >= 0; all finite.  The p, m, v and scale arrays
+ * of a call must not overlap each other or the gradients
+ * (BSFP8_ERR_INVALID_ARG).  Infinities and NaN in gradients spread to p, m and
+ * v; with FP8 states to the whole block of 128 (scale byte 255): use found_inf.
+ */
+bsfp8_status adamw_step(const bsfp8_adamw_tensor* tensors, int64_t count, bsfp8_out p_type, bsfp8_out g_type,
+                        bsfp8_state state, const bsfp8_adamw_args* args, hipStream_t stream);
+
+/*
  * bsfp8_status_string -- the name of a status code ("BSFP8_OK", ...;
  * "BSFP8_ERR_UNKNOWN" for a value that is not a bsfp8_status), in static
  * storage owned by the library; never NULL.  The status values follow the
