@@ -14,7 +14,7 @@
 //
 // Scale bytes lie in words of four K blocks, [ceil(K / 512)][scale rows][4]: a
 // lane reads one word per 512 K, and the 32 rows of a tile lie side by side.
-#include "big_tile.h"
+#include "gemm_block128.h"
 
 namespace bsfp8 {
 
@@ -22,9 +22,6 @@ namespace {
 
 using namespace big_tile;
 typedef int v8i __attribute__((ext_vector_type(8)));
-
-template <int FMT>
-constexpr int mfma_fmt() { return FMT == BSFP8_E4M3 ? 0 : 1; }
 
 // Eight FP8 codes (two dwords) times the scale -> eight bf16 (four dwords),
 // exactly as long as the products are normal bf16.
@@ -72,14 +69,6 @@ __device__ __forceinline__ v16f step64(const u32x4& x0, const u32x4& x1, const u
     }
 }
 
-// One operand's scales: byte j of word (g, r) is the scale of K block 4 g + j
-// of scale row r; shift is 0 (one scale row per row) or 7 (one per 128 rows).
-struct ScaleRows {
-    const uint32_t* words;
-    int64_t rows;
-    int shift;
-};
-
 // Narrow form: one workgroup per 32 x 32 output tile, its four waves taking
 // contiguous ranges of the K blocks.  Each load instruction reads whole
 // 128-byte row segments (8 rows x 128 bytes), which pass through the wave's
@@ -88,6 +77,8 @@ struct ScaleRows {
 // four partial sums are added in a fixed order.
 constexpr int kNarrowDepth = 2;
 constexpr int kNarrowWaves = 4;
+constexpr int64_t kNarrowMaxM = 64;          // rows up to which it is always used
+constexpr int64_t kBigTiles = 64;            // 256 x 256 tiles from which the large form is used
 
 template <int AF, int BF, int OUT>
 __global__ __launch_bounds__(64 * kNarrowWaves, 2) void gemm_block128_narrow_kernel(
@@ -216,6 +207,8 @@ hipError_t launch_gemm_block128(int64_t M, int64_t N, int64_t K, int a_fmt, cons
                                 int b_block_rows, int out, void* d, int64_t ldd, const Epilogue& ep,
                                 hipStream_t stream) {
     const ScaleRows sa = scale_rows(a_scales, M, a_block_rows), sb = scale_rows(b_scales, N, b_block_rows);
+    if (out != BSFP8_OUT_F32 && M > kNarrowMaxM && ((M + 255) / 256) * ((N + 255) / 256) >= kBigTiles)
+        return launch_gemm_block128_big(M, N, K, a_fmt, a, sa, b_fmt, b, sb, out, d, ldd, ep, stream);
     if (a_fmt == BSFP8_E4M3 && b_fmt == BSFP8_E4M3)
         return launch_typed<BSFP8_E4M3, BSFP8_E4M3>(M, N, K, a, sa, b, sb, out, d, ldd, ep, stream);
     if (a_fmt == BSFP8_E4M3)
