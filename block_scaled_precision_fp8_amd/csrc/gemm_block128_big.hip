@@ -1,18 +1,25 @@
-// gemm_block128_big.hip -- the 256 x 256-tile form of the block-of-128 FP8 GEMM (gfx950).
+// gemm_block128_big.hip -- the tiled forms of the block-of-128 FP8 GEMM (gfx950).
 //
-// One workgroup per CU, four waves of 128 x 128 (4 x 4 MFMA tiles of 32 x 32,
-// 256 FP32 accumulators per lane in the accumulation registers).  K advances in
-// stages of 128, one scale block: 256 rows x 128 bytes of A and of B (64 KB) by
-// direct global-to-LDS loads of whole 128-byte lines, in two buffers.  The
-// scale words of four stages (512 rows x 4 bytes) come the same way, a group
-// ahead.  The main loop is volatile inline assembly, so that loads, fragment
-// reads and MFMAs interleave in program order; the waits are explicit.
+// A workgroup of four waves (2 x 2) computes tiles of 64 TA x 64 TB outputs,
+// each wave TA x TB MFMA tiles of 32 x 32.  K advances in stages of 128, one
+// scale block: the tile's rows x 128 bytes of A and of B come by direct
+// global-to-LDS loads of whole 128-byte lines into one of two buffers; the scale
+// words of four stages come the same way, a group ahead.  The main loop is
+// volatile inline assembly, so that loads, fragment reads and MFMAs interleave
+// in program order; the waits are explicit.
 //
-// 16-bit outputs: v_mfma_scale_f32_32x32x64_f8f6f4 with the rows' E8M0 bytes,
-// two steps of 64 K per stage.  FP32 output: the codes, times their scale, are
-// widened to bf16 (exact) a quarter step ahead of their MFMAs
-// (v_mfma_f32_32x32x16_bf16, 24 fraction bits instead of 13), between the MFMAs
-// of the quarter before.
+// The schedule of a stage (2 TA TB MFMA slots) is what carries the kernel: the
+// fragments of its second step are read in its first slots, so that a first
+// barrier can free its buffer a quarter of the way through and the loads of
+// stage s + 2 can start there, spread over the rest of the stage; they have the
+// whole next stage but its tail to land, until that stage's second barrier
+// publishes them.  One barrier for both, with the loads behind it, measured
+// 2380 (FFN 16384 x 14336 x 4096) and 2550 TFLOP/s (8192^3) against 2540 and
+// 2780; finer variations of the slots changed nothing.
+//
+// With more tiles than workgroups the grid is persistent: the loads run on into
+// the next tile's first stages while the last ones of this tile are computed
+// and written, so only the first tile of a workgroup waits for memory.
 #include "gemm_block128.h"
 
 namespace bsfp8 {
@@ -25,11 +32,7 @@ typedef __attribute__((address_space(3))) void lds_void;
 
 constexpr int kThreads = 256;
 constexpr int kRowBytes = 128;
-constexpr int kOperandBytes = 256 * kRowBytes;        // 32 KB
-constexpr int kStageBytes = 2 * kOperandBytes;        // 64 KB
-constexpr int kScaleLds = 2 * kStageBytes;            // two groups of 512 words after the stages
-constexpr int kScaleGroupBytes = 512 * 4;
-constexpr int kLdsBytes = kScaleLds + 2 * kScaleGroupBytes;
+constexpr int kStripBytes = 4096;     // epilogue staging per wave
 
 template <int OFF>
 __device__ __forceinline__ void lds_read4(uint32_t& v, uint32_t addr) {
@@ -44,89 +47,116 @@ __device__ __forceinline__ void mfma_scaled(v16f& acc, const u32x8& x, const u32
         : "+a"(acc)
         : "v"(x), "v"(y), "v"(sx), "v"(sy), "i"(SEL & 1), "i"(SEL >> 1), "i"(CB), "i"(BG));
 }
-__device__ __forceinline__ void mfma_bf16_k16(v16f& acc, const u32x4& x, const u32x4& y) {
-    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(x), "v"(y));
-}
-// Two codes (half HI of w) times the scale s -> two bf16, in place in the stream.
-template <int FMT, int HI>
-__device__ __forceinline__ uint32_t widen2(uint32_t w, float s) {
-    uint32_t d;
-    if constexpr (FMT == BSFP8_E4M3) {
-        if constexpr (HI) asm volatile("v_cvt_scalef32_pk_bf16_fp8 %0, %1, %2 op_sel:[1,0,0]" : "=v"(d) : "v"(w), "v"(s));
-        else asm volatile("v_cvt_scalef32_pk_bf16_fp8 %0, %1, %2" : "=v"(d) : "v"(w), "v"(s));
-    } else {
-        if constexpr (HI) asm volatile("v_cvt_scalef32_pk_bf16_bf8 %0, %1, %2 op_sel:[1,0,0]" : "=v"(d) : "v"(w), "v"(s));
-        else asm volatile("v_cvt_scalef32_pk_bf16_bf8 %0, %1, %2" : "=v"(d) : "v"(w), "v"(s));
-    }
-    return d;
-}
 
-template <int AF, int BF, int OUT, bool STAGE16>
-__global__ __launch_bounds__(kThreads, 1) void gemm_block128_big_kernel(
+template <int TA, int TB>
+struct Tile {
+    static constexpr int ROWS_A = 64 * TA, ROWS_B = 64 * TB;
+    static constexpr int A_BYTES = ROWS_A * kRowBytes, STAGE_BYTES = A_BYTES + ROWS_B * kRowBytes;
+    static constexpr int SCALE_GROUP = (ROWS_A + ROWS_B) * 4;       // words of four K blocks
+    static constexpr int SCALES = 2 * STAGE_BYTES;                  // LDS offsets
+    static constexpr int STRIPS = SCALES + 2 * SCALE_GROUP;
+    static constexpr int LDS_BYTES = STRIPS + 4 * kStripBytes;
+    // slots of a stage: MFMAs per step, fragment reads per step, direct loads per stage and wave
+    static constexpr int NM = TA * TB, NR = 2 * (TA + TB), NL = 2 * (TA + TB);
+    static constexpr int RPS = NR / (NM / 2);                       // reads per slot
+    static constexpr int FREE = NM / 2 - 1;                         // first barrier: after this slot
+    static constexpr int READY = NM + NM / 4;                       // second barrier
+    static constexpr int load_slot(int k) {
+        return k < NL / 2 ? NM / 2 + k * (NM / 2) / (NL / 2) : NM + (k - NL / 2) * NM / (NL / 2);
+    }
+    static constexpr int newer() {                                  // loads issued before READY's wait
+        int c = 0;
+        for (int k = 0; k < NL; ++k) c += load_slot(k) <= READY ? 1 : 0;
+        return c;
+    }
+    static constexpr int STORES = TA * TB * 2;                      // of the constant-count epilogue
+};
+
+// FAST: 16-bit output without C, every chunk of 8 outputs whole and aligned:
+// the epilogue is a fixed number of range-checked buffer stores, so the loop
+// can leave them in flight.
+template <int AF, int BF, int OUT, int TA, int TB, bool FAST>
+__global__ __launch_bounds__(kThreads, 1) void gemm_block128_tile_kernel(
     int M, int N, int K, const uint8_t* __restrict__ A, ScaleRows sA, const uint8_t* __restrict__ B, ScaleRows sB,
     void* __restrict__ D, int64_t ldd, Epilogue ep, int tiles_m, int tiles_n, int vec_ok) {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kLdsBytes];
+    using T = Tile<TA, TB>;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS_BYTES];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave & 1;
     const int wn = wave >> 1;
-    int tm, tn;
-    map_tile(blockIdx.x, tiles_m, tiles_n, 8, &tm, &tn);
-    const int m0 = tm * 256;
-    const int n0 = tn * 256;
-    const int nst = (K + 127) >> 7;
+    const int tiles = tiles_m * tiles_n;
+    const int real = (K + 127) >> 7;                 // stages that hold K values
+    const int nst = (real + 1) & ~1;                 // pairs, so that a stage's buffer is compile-time
     const int ngr = (nst + 3) >> 2;
 
+    // The loader: two stages ahead of the MFMAs, running on into the next tile.
     // The resources start at the tile's first row and end after its last row
-    // inside the matrix: rows past the edge read as zero, offsets stay below
-    // 256 K < 2^31.
-    const int rows_a = min(256, M - m0);
-    const int rows_b = min(256, N - n0);
-    const __amdgpu_buffer_rsrc_t rs_a = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(A) + static_cast<int64_t>(m0) * K, 0, rows_a * K, 0x00020000);
-    const __amdgpu_buffer_rsrc_t rs_b = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(B) + static_cast<int64_t>(n0) * K, 0, rows_b * K, 0x00020000);
-
-    // Direct loads: load j (0..15) of wave w fills rows 8 g .. 8 g + 7 of operand
-    // j & 1 (A, B), g = 4 (j >> 1) + w.  Lane l brings row 8 g + l / 8 and the
-    // chunk that belongs at position l % 8: chunk c of row R sits at
-    // c ^ ((R >> 1) & 7).  Chunks and stages past K are given an out-of-range
-    // offset and read as zero.
+    // inside the matrix: rows past the edge read as zero (all of them past the
+    // last tile), offsets stay below 256 K < 2^31.
+    int l_tile = blockIdx.x, l_stage = 0;
+    __amdgpu_buffer_rsrc_t rs_a, rs_b;
+    auto aim = [&]() {
+        int tm = 0, tn = 0;
+        const bool any = l_tile < tiles;
+        if (any) map_tile(l_tile, tiles_m, tiles_n, 8, &tm, &tn);
+        const int m0 = tm * T::ROWS_A, n0 = tn * T::ROWS_B;
+        rs_a = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(A) + static_cast<int64_t>(m0) * K, 0,
+                                                 any ? min(T::ROWS_A, M - m0) * K : 0, 0x00020000);
+        rs_b = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(B) + static_cast<int64_t>(n0) * K, 0,
+                                                 any ? min(T::ROWS_B, N - n0) * K : 0, 0x00020000);
+    };
+    auto advance = [&]() {
+        if (++l_stage == nst) {
+            l_stage = 0;
+            l_tile += gridDim.x;
+            aim();
+        }
+    };
+    // Direct load j of wave w fills rows 8 g .. 8 g + 7 of A (j < 2 TA) or B,
+    // g = 4 (j or j - 2 TA) + w.  Lane l brings row 8 g + l / 8 and the chunk that
+    // belongs at position l % 8: chunk c of row R sits at c ^ ((R >> 1) & 7).
+    // Chunks past K are given an out-of-range offset and read as zero.
     const int drow = lane >> 3;
     const int dchunk = (lane & 7) ^ (((8 * wave + drow) >> 1) & 7);
     const uint32_t dma_row = static_cast<uint32_t>((8 * wave + drow) * K + dchunk * 16);
     const uint32_t dma_grp = static_cast<uint32_t>(32 * K);
-    auto dma_one = [&](auto J, int stage, auto BUF) {
+    auto dma_one = [&](auto J, auto BUF) {
         constexpr int j = J;
         constexpr int buf = BUF;
-        constexpr int gi = j >> 1;
-        const uint32_t vo = stage * 128 + dchunk * 16 < K ? dma_row + gi * dma_grp : 0x80000000u;
-        lds_void* dst = (lds_void*)(lds + buf * kStageBytes + (j & 1) * kOperandBytes + (4 * gi + wave) * 1024);
-        if constexpr ((j & 1) == 0)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, dst, 16, vo, stage * 128, 0, 0);
+        // A and B in turn as long as both have loads left
+        constexpr int both = 4 * (TA < TB ? TA : TB);
+        constexpr bool is_a = j < both ? (j & 1) == 0 : TA > TB;
+        constexpr int gi = j < both ? j >> 1 : j - both / 2;
+        const uint32_t vo = l_stage * 128 + dchunk * 16 < K ? dma_row + gi * dma_grp : 0x80000000u;
+        lds_void* dst = (lds_void*)(lds + buf * T::STAGE_BYTES + (is_a ? 0 : T::A_BYTES) + (4 * gi + wave) * 1024);
+        if constexpr (is_a)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, dst, 16, vo, l_stage * 128, 0, 0);
         else
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, dst, 16, vo, stage * 128, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, dst, 16, vo, l_stage * 128, 0, 0);
     };
-    // Scale words of a group: this wave's 64 rows of A (q = 0) or B (q = 1);
-    // rows past the edge and groups past the end take one that exists.
-    const int64_t sra = min(m0 + 64 * wave + lane, M - 1) >> sA.shift;
-    const int64_t srb = min(n0 + 64 * wave + lane, N - 1) >> sB.shift;
-    auto scale_dma = [&](int group, int q) {
-        const int g = min(group, ngr - 1);
-        const uint32_t* src = q == 0 ? sA.words + g * sA.rows + sra : sB.words + g * sB.rows + srb;
-        lds_void* dst = (lds_void*)(lds + kScaleLds + (group & 1) * kScaleGroupBytes + q * 1024 + wave * 256);
-        __builtin_amdgcn_global_load_lds(src, dst, 4, 0, 0);
+    // Scale words of a group of the tile at (m0, n0): wave w brings rows
+    // 16 TA w .. of A (q = 0), 16 TB w .. of B (q = 1); rows past the edge take
+    // one that exists.
+    int slot = 0;                                    // LDS slot of the group in use
+    auto scale_dma = [&](int m0, int n0, int group, int to, int q) {
+        const int per = q == 0 ? 16 * TA : 16 * TB;
+        const int row = min((q == 0 ? m0 : n0) + per * wave + min(lane, per - 1), (q == 0 ? M : N) - 1);
+        const uint32_t* src = q == 0 ? sA.words + group * sA.rows + (row >> sA.shift)
+                                     : sB.words + group * sB.rows + (row >> sB.shift);
+        lds_void* dst = (lds_void*)(lds + T::SCALES + to * T::SCALE_GROUP + (q == 0 ? 0 : T::ROWS_A * 4) + wave * per * 4);
+        if (lane < per) __builtin_amdgcn_global_load_lds(src, dst, 4, 0, 0);
     };
 
     // Fragment reads of step ks: lane (frag_row r, half h) reads chunks 4 ks + h
-    // and 4 ks + 2 + h of rows wm 128 + 32 t + r (A), wn 128 + 32 t + r (B).
+    // and 4 ks + 2 + h of rows wm 32 TA + 32 t + r (A), wn 32 TB + 32 t + r (B).
     const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_byte*)lds));
     const int frag_row = lane & 31;
     const int half = lane >> 5;
     const int sw = (frag_row >> 1) & 7;
-    uint32_t rd_a[2][2][2], rd_b[2][2][2];       // [buffer][ks][low, high chunk]
+    uint32_t rd_a[2][2][2], rd_b[2][2][2];           // [buffer][ks][low, high chunk]
 #pragma unroll
     for (int bf = 0; bf < 2; ++bf)
 #pragma unroll
@@ -134,152 +164,279 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_block128_big_kernel(
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const uint32_t pos = static_cast<uint32_t>(((4 * ks + 2 * q + half) ^ sw) * 16);
-                rd_a[bf][ks][q] = lds0 + bf * kStageBytes + (wm * 128 + frag_row) * kRowBytes + pos;
-                rd_b[bf][ks][q] = lds0 + bf * kStageBytes + kOperandBytes + (wn * 128 + frag_row) * kRowBytes + pos;
+                rd_a[bf][ks][q] = lds0 + bf * T::STAGE_BYTES + (wm * 32 * TA + frag_row) * kRowBytes + pos;
+                rd_b[bf][ks][q] = lds0 + bf * T::STAGE_BYTES + T::A_BYTES + (wn * 32 * TB + frag_row) * kRowBytes + pos;
             }
 
-    v16f acc[4][4];
+    v16f acc[TB][TA];
+    // zeros by the matrix core (0 x 0 + 0), straight into the accumulation
+    // registers: through VGPRs they cost the main loop's registers
+    auto clear = [&]() {
+        u32x4 z = {0u, 0u, 0u, 0u};
+        asm volatile("s_nop 4" : "+v"(z));
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < TB; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = v16f{};
+            for (int j = 0; j < TA; ++j) asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %1, 0" : "=a"(acc[i][j]) : "v"(z));
+        asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+    };
+    clear();
 
-    struct Frag { u32x4 xl[4], xh[4], yl[4], yh[4]; };
+    struct Frag { u32x4 xl[TB], xh[TB], yl[TA], yh[TA]; };
     Frag fr[2];
-    // read piece R (0..15) of step KS of the stage in buffer BUF
+    // read piece R (0 .. NR - 1) of step KS of the stage in buffer BUF: B first
     auto read_one = [&](auto R, Frag& dst, auto BUF, auto KS) {
         constexpr int r = R;
-        constexpr int t = r >> 2;
-        constexpr int which = r & 3;
+        constexpr int t = (r < 2 * TB ? r : r - 2 * TB) >> 1;
+        constexpr int hi = r & 1;
         constexpr int off = t * 32 * kRowBytes;
-        if constexpr (which == 0) lds_read16<off>(dst.xl[t], rd_b[BUF][KS][0]);
-        if constexpr (which == 1) lds_read16<off>(dst.xh[t], rd_b[BUF][KS][1]);
-        if constexpr (which == 2) lds_read16<off>(dst.yl[t], rd_a[BUF][KS][0]);
-        if constexpr (which == 3) lds_read16<off>(dst.yh[t], rd_a[BUF][KS][1]);
+        if constexpr (r < 2 * TB) lds_read16<off>(hi ? dst.xh[t] : dst.xl[t], rd_b[BUF][KS][hi]);
+        else lds_read16<off>(hi ? dst.yh[t] : dst.yl[t], rd_a[BUF][KS][hi]);
     };
     // the scale words of this lane's rows: nxt as read from LDS, cur in use
-    uint32_t nxt[8], cur[8];
-    const uint32_t srd_a = lds0 + kScaleLds + (wm * 128 + frag_row) * 4;
-    const uint32_t srd_b = lds0 + kScaleLds + 1024 + (wn * 128 + frag_row) * 4;
-    auto read_scale = [&](auto T, int group) {
-        constexpr int t = T;
-        const uint32_t o = (group & 1) * kScaleGroupBytes;
-        if constexpr (t < 4) lds_read4<t * 128>(nxt[t], srd_a + o);
-        else lds_read4<(t - 4) * 128>(nxt[t], srd_b + o);
+    uint32_t nxt[TA + TB], cur[TA + TB];
+    const uint32_t srd_a = lds0 + T::SCALES + (wm * 32 * TA + frag_row) * 4;
+    const uint32_t srd_b = lds0 + T::SCALES + T::ROWS_A * 4 + (wn * 32 * TB + frag_row) * 4;
+    auto read_scale = [&](auto I, int from) {
+        constexpr int t = I;
+        if constexpr (t < TA) lds_read4<t * 128>(nxt[t], srd_a + from * T::SCALE_GROUP);
+        else lds_read4<(t - TA) * 128>(nxt[t], srd_b + from * T::SCALE_GROUP);
+    };
+    auto name_scales = [&](uint32_t (&v)[TA + TB]) {
+#pragma unroll
+        for (int t = 0; t < TA + TB; ++t) asm volatile("" : "+v"(v[t]));
     };
     // bytes past the last K block (their codes are zero) become a unit scale
-    const uint32_t used = (nst & 3) ? (1u << (8 * (nst & 3))) - 1u : 0xFFFFFFFFu;
+    const uint32_t used = (real & 3) ? (1u << (8 * (real & 3))) - 1u : 0xFFFFFFFFu;
     auto take_scales = [&](int group) {
         const uint32_t keep = group == ngr - 1 ? used : 0xFFFFFFFFu;
 #pragma unroll
-        for (int t = 0; t < 8; ++t) cur[t] = (nxt[t] & keep) | (0x7F7F7F7Fu & ~keep);
+        for (int t = 0; t < TA + TB; ++t) cur[t] = (nxt[t] & keep) | (0x7F7F7F7Fu & ~keep);
         // VALU writes settle before an MFMA of the assembly reads them
-        asm volatile("s_nop 4" : "+v"(cur[0]), "+v"(cur[1]), "+v"(cur[2]), "+v"(cur[3]), "+v"(cur[4]), "+v"(cur[5]),
-                                 "+v"(cur[6]), "+v"(cur[7]));
+        name_scales(cur);
+        asm volatile("s_nop 4");
     };
 
     constexpr auto C0 = std::integral_constant<int, 0>{};
     constexpr auto C1 = std::integral_constant<int, 1>{};
 
-    // Prologue: stage 0, the first two scale groups and stage 1 on their way.
-    static_for<16>([&](auto J) { dma_one(J, 0, C0); });
-    scale_dma(0, 0);
-    scale_dma(0, 1);
-    static_for<16>([&](auto J) { dma_one(J, 1, C1); });
-    asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
-    lds_wait_barrier();
-    static_for<16>([&](auto R) { read_one(R, fr[0], C0, C0); });
-    static_for<8>([&](auto T) { read_scale(T, 0); });
-    lds_wait();
-    take_scales(0);
+    int tile = blockIdx.x, tm, tn;
+    map_tile(tile, tiles_m, tiles_n, 8, &tm, &tn);
+    int m0 = tm * T::ROWS_A, n0 = tn * T::ROWS_B;
 
-    // One K step on fragment set KS: MFMAs, with the next step's fragment reads
-    // in their shadows.  Step 1 follows the barrier that publishes stage s + 1
-    // and frees this stage's buffer: it reads stage s + 1's first fragments and
-    // issues the direct loads of stage s + 2, one per MFMA.
-    auto kstep = [&](int s, auto CB_, auto KS, auto U) {
-        constexpr int cb = CB_;
-        constexpr int ks = KS;
-        constexpr int u = U;                  // stage within its scale group
-        const Frag& f = fr[ks];
-        Frag& g = fr[ks ^ 1];
-        constexpr auto rbuf = std::integral_constant<int, ks == 1 ? (cb ^ 1) : cb>{};
-        constexpr auto rks = std::integral_constant<int, ks ^ 1>{};
-        static_for<16>([&](auto J) {
-            constexpr int j = J;
-            constexpr int ti = j >> 2, tj = j & 3;
-            const u32x8 x = __builtin_shufflevector(f.xl[ti], f.xh[ti], 0, 1, 2, 3, 4, 5, 6, 7);
-            const u32x8 y = __builtin_shufflevector(f.yl[tj], f.yh[tj], 0, 1, 2, 3, 4, 5, 6, 7);
-            mfma_scaled<u, mfma_fmt<BF>(), mfma_fmt<AF>()>(acc[ti][tj], x, y, cur[4 + ti], cur[tj]);
-            read_one(J, g, rbuf, rks);
-            if constexpr (ks == 1) {
-                dma_one(J, s + 2, CB_);
-                if constexpr (u == 3 && j < 8) read_scale(J, (s >> 2) + 1);
-                if constexpr (u == 0 && j == 8) scale_dma((s >> 2) + 1, 0);
-                if constexpr (u == 0 && j == 9) scale_dma((s >> 2) + 1, 1);
-            }
-        });
-    };
-    auto run_stage = [&](int s, auto U) {
-        constexpr auto cb = std::integral_constant<int, U & 1>{};
-        lds_wait();
-        if constexpr (U == 0) {
-            if (s > 0) take_scales(s >> 2);
+    // Prologue: stage 0, the first scale group and stage 1 on their way.
+    aim();
+    static_for<T::NL>([&](auto J) { dma_one(J, C0); });
+    advance();
+    scale_dma(m0, n0, 0, 0, 0);
+    scale_dma(m0, n0, 0, 0, 1);
+    static_for<T::NL>([&](auto J) { dma_one(J, C1); });
+    advance();
+    asm volatile("s_waitcnt vmcnt(%0)" :: "i"(T::NL) : "memory");
+    lds_wait_barrier();
+    static_for<T::NR>([&](auto R) { read_one(R, fr[0], C0, C0); });
+    static_for<TA + TB>([&](auto I) { read_scale(I, 0); });
+
+    bool stores = false;                             // an epilogue's stores may be in flight
+    for (;;) {
+        int nm0 = m0, nn0 = n0;
+        const bool more = tile + static_cast<int>(gridDim.x) < tiles;
+        if (more) {
+            map_tile(tile + gridDim.x, tiles_m, tiles_n, 8, &tm, &tn);
+            nm0 = tm * T::ROWS_A;
+            nn0 = tn * T::ROWS_B;
         }
-        kstep(s, cb, C0, U);
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        lds_wait_barrier();
-        kstep(s, cb, C1, U);
-    };
-    for (int s = 0; s < nst; s += 4) {
-        run_stage(s, C0);
-        if (s + 1 < nst) run_stage(s + 1, C1);
-        if (s + 2 < nst) run_stage(s + 2, std::integral_constant<int, 2>{});
-        if (s + 3 < nst) run_stage(s + 3, std::integral_constant<int, 3>{});
+        auto run_stage = [&](int s, auto U) {
+            constexpr int u = U;                     // stage within its scale group
+            constexpr auto cb = std::integral_constant<int, u & 1>{};
+            constexpr auto nb = std::integral_constant<int, (u & 1) ^ 1>{};
+            lds_wait();
+            if constexpr (u == 0) {
+                take_scales(s >> 2);
+            }
+            const bool group_end = u == 3 || (u == 1 && s + 1 == nst);
+            static_for<2 * T::NM>([&](auto N_) {
+                constexpr int n = N_;
+                constexpr int ks = n / T::NM;
+                constexpr int ti = n % T::NM / TA, tj = n % TA;
+                const Frag& f = fr[ks];
+                const u32x8 x = __builtin_shufflevector(f.xl[ti], f.xh[ti], 0, 1, 2, 3, 4, 5, 6, 7);
+                const u32x8 y = __builtin_shufflevector(f.yl[tj], f.yh[tj], 0, 1, 2, 3, 4, 5, 6, 7);
+                mfma_scaled<u, mfma_fmt<BF>(), mfma_fmt<AF>()>(acc[ti][tj], x, y, cur[TA + ti], cur[tj]);
+                if constexpr (n * T::RPS < T::NR)
+                    static_for<T::RPS>([&](auto Q) { read_one(std::integral_constant<int, n * T::RPS + Q>{}, fr[1], cb, C1); });
+                if constexpr (n == T::FREE) lds_wait_barrier();
+                static_for<T::NL>([&](auto J) {
+                    if constexpr (T::load_slot(J) == n) dma_one(J, cb);
+                });
+                if constexpr (n == T::READY) {
+                    // stage s + 1 has landed once only the loads issued in this
+                    // stage (and, in a tile's first, the last tile's stores,
+                    // which are younger than it) are outstanding
+                    if (u == 0 && stores) {
+                        asm volatile("s_waitcnt vmcnt(%0)" :: "i"(T::newer() + T::STORES) : "memory");
+                        stores = false;
+                    } else {
+                        asm volatile("s_waitcnt vmcnt(%0)" :: "i"(T::newer()) : "memory");
+                    }
+                    lds_wait_barrier();
+                }
+                if constexpr (n > T::READY && (n - T::READY - 1) * T::RPS < T::NR)
+                    static_for<T::RPS>([&](auto Q) {
+                        read_one(std::integral_constant<int, (n - T::READY - 1) * T::RPS + Q>{}, fr[0], nb, C0);
+                    });
+                // the next group's scales, or the next tile's first: loaded in a
+                // group's first stage, read in its last
+                if constexpr (u == 0 && n == T::READY + 1) {
+                    const bool in = (s >> 2) + 1 < ngr;
+                    scale_dma(in ? m0 : nm0, in ? n0 : nn0, in ? (s >> 2) + 1 : 0, slot ^ 1, 0);
+                    scale_dma(in ? m0 : nm0, in ? n0 : nn0, in ? (s >> 2) + 1 : 0, slot ^ 1, 1);
+                }
+                if constexpr ((u & 1) && n == 2 * T::NM - 2) {
+                    if (group_end) {
+                        slot ^= 1;
+                        static_for<TA + TB>([&](auto I) { read_scale(I, slot); });
+                    }
+                }
+            });
+            advance();
+        };
+        for (int s = 0; s < nst; s += 4) {
+            run_stage(s, C0);
+            run_stage(s + 1, C1);
+            if (s + 2 < nst) {
+                run_stage(s + 2, std::integral_constant<int, 2>{});
+                run_stage(s + 3, std::integral_constant<int, 3>{});
+            }
+        }
+        // The next tile's first fragments and scales are in their registers
+        // before the compiler's own code runs (it may move them); MFMA results
+        // must settle before the accumulation registers are read.
+        lds_wait();
+        asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < TB; ++i)
+#pragma unroll
+            for (int j = 0; j < TA; ++j) asm volatile("" : "+a"(acc[i][j]));
+
+        // Epilogue, each wave by itself through its own strip of LDS, so that
+        // stores write whole lines.  acc[ti][tj][4 q + e] is row 32 tj +
+        // frag_row, column 32 ti + 8 q + 4 half + e of the wave's part.  Chunk c
+        // (16 bytes) of strip row R sits at c ^ ((R >> 1) & 7).
+        // (The lane is opaque here, so that the epilogue's addresses are not kept
+        // in registers through the main loop.)
+        uint8_t* strip = lds + T::STRIPS + wave * kStripBytes;
+        const int mw = m0 + wm * 32 * TA, nw = n0 + wn * 32 * TB;
+        int el = lane;
+        asm volatile("" : "+v"(el));
+        const int srow = el >> 3, schunk = el & 7;
+        uint8_t* put = strip + (el & 31) * 128;
+        const int psw = (el >> 1) & 7, phalf = el >> 5;
+        if constexpr (FAST) {
+            // strips of 32 rows x 64 columns of 16-bit outputs
+            const __amdgpu_buffer_rsrc_t rs_d = __builtin_amdgcn_make_buffer_rsrc(
+                static_cast<uint16_t*>(D) + static_cast<int64_t>(m0) * ldd, 0,
+                min(T::ROWS_A, M - m0) * static_cast<int>(ldd) * 2, 0x00020000);
+#pragma unroll
+            for (int tj = 0; tj < TA; ++tj)
+#pragma unroll
+                for (int tp = 0; tp < TB / 2; ++tp) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const v16f& a = acc[2 * tp + t][tj];
+                            const uint32_t h0 = to_half_bits<OUT>(ep.alpha * a[4 * q + 0]);
+                            const uint32_t h1 = to_half_bits<OUT>(ep.alpha * a[4 * q + 1]);
+                            const uint32_t h2 = to_half_bits<OUT>(ep.alpha * a[4 * q + 2]);
+                            const uint32_t h3 = to_half_bits<OUT>(ep.alpha * a[4 * q + 3]);
+                            *reinterpret_cast<uint2*>(put + (((4 * t + q) ^ psw) << 4) + 8 * phalf) =
+                                make_uint2(h0 | (h1 << 16), h2 | (h3 << 16));
+                        }
+                    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int R = 8 * i + srow;
+                        const u32x4 w = *reinterpret_cast<const u32x4*>(strip + R * 128 + ((schunk ^ ((R >> 1) & 7)) << 4));
+                        const int col = nw + 64 * tp + 8 * schunk;
+                        const uint32_t off = col < N ? static_cast<uint32_t>(((mw - m0 + 32 * tj + R) * static_cast<int>(ldd) + col) * 2)
+                                                     : 0x80000000u;
+                        __builtin_amdgcn_raw_buffer_store_b128(w, rs_d, off, 0, 0);
+                    }
+                    __builtin_amdgcn_wave_barrier();
+                }
+            stores = true;
+        } else {
+            // strips of 32 rows x 32 columns in FP32; alpha, beta C and the
+            // conversion row by row, masked at the edges
+#pragma unroll
+            for (int tj = 0; tj < TA; ++tj)
+#pragma unroll
+                for (int ti = 0; ti < TB; ++ti) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const v16f& a = acc[ti][tj];
+                        *reinterpret_cast<float4*>(put + (((2 * q + phalf) ^ psw) << 4)) =
+                            make_float4(a[4 * q + 0], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
+                    }
+                    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int R = 8 * i + srow;
+                        const float4 v = *reinterpret_cast<const float4*>(strip + R * 128 + ((schunk ^ ((R >> 1) & 7)) << 4));
+                        const float a4[4] = {v.x, v.y, v.z, v.w};
+                        finish_row_chunk<OUT, 4>(D, ldd, ep, mw + 32 * tj + R, nw + 32 * ti + 4 * schunk, M, N, vec_ok, a4);
+                    }
+                    __builtin_amdgcn_wave_barrier();
+                }
+            // a masked store may not have been issued: none is left in flight
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+        if (!more) break;
+        clear();
+        tile += gridDim.x;
+        m0 = nm0;
+        n0 = nn0;
     }
-    // no direct load may still be writing LDS when the epilogue reuses it, and
-    // the last step's reads, which have no consumer, are named after the wait
-    // so that their registers are not reused while in flight
+    // no direct load may still be writing LDS when the workgroup ends, and the
+    // last reads, which have no consumer, are named after the wait so that
+    // their registers are not reused while in flight
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        asm volatile("" :: "v"(fr[q].xl[0]), "v"(fr[q].xl[1]), "v"(fr[q].xl[2]), "v"(fr[q].xl[3]),
-                           "v"(fr[q].xh[0]), "v"(fr[q].xh[1]), "v"(fr[q].xh[2]), "v"(fr[q].xh[3]));
-        asm volatile("" :: "v"(fr[q].yl[0]), "v"(fr[q].yl[1]), "v"(fr[q].yl[2]), "v"(fr[q].yl[3]),
-                           "v"(fr[q].yh[0]), "v"(fr[q].yh[1]), "v"(fr[q].yh[2]), "v"(fr[q].yh[3]));
-    }
-    asm volatile("" :: "v"(nxt[0]), "v"(nxt[1]), "v"(nxt[2]), "v"(nxt[3]), "v"(nxt[4]), "v"(nxt[5]), "v"(nxt[6]),
-                       "v"(nxt[7]));
-    // MFMA results must settle before the accumulation registers are read
-    asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7"
-                 : "+a"(acc[0][0]), "+a"(acc[0][1]), "+a"(acc[0][2]), "+a"(acc[0][3]),
-                   "+a"(acc[1][0]), "+a"(acc[1][1]), "+a"(acc[1][2]), "+a"(acc[1][3]),
-                   "+a"(acc[2][0]), "+a"(acc[2][1]), "+a"(acc[2][2]), "+a"(acc[2][3]),
-                   "+a"(acc[3][0]), "+a"(acc[3][1]), "+a"(acc[3][2]), "+a"(acc[3][3]));
-    NoScale none;
-    epilogue<OUT, STAGE16>(acc, lds, wave, lane, m0, n0, M, N, D, ldd, ep, vec_ok, none);
+    for (int t = 0; t < TB; ++t) asm volatile("" :: "v"(fr[0].xl[t]), "v"(fr[0].xh[t]));
+#pragma unroll
+    for (int t = 0; t < TA; ++t) asm volatile("" :: "v"(fr[0].yl[t]), "v"(fr[0].yh[t]));
+    name_scales(nxt);
 }
 
-template <int AF, int BF, int OUT, bool STAGE16>
+// Persistent workgroups: one per CU.
+constexpr int64_t kPersistent = 256;
+
+template <int AF, int BF, int OUT, int TA, int TB, bool FAST>
 hipError_t launch(int64_t M, int64_t N, int64_t K, const uint8_t* a, const ScaleRows& sa, const uint8_t* b,
                   const ScaleRows& sb, void* d, int64_t ldd, const Epilogue& ep, hipStream_t stream) {
-    const int tm = static_cast<int>((M + 255) / 256), tn = static_cast<int>((N + 255) / 256);
-    hipLaunchKernelGGL((gemm_block128_big_kernel<AF, BF, OUT, STAGE16>),
-                       dim3(static_cast<uint32_t>(tm) * static_cast<uint32_t>(tn)), dim3(kThreads), 0, stream,
-                       static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), a, sa, b, sb, d, ldd, ep, tm, tn,
-                       vec16_ok(OUT, d, ldd, ep));
+    const int64_t tm = (M + 64 * TA - 1) / (64 * TA), tn = (N + 64 * TB - 1) / (64 * TB);
+    const int64_t grid = tm * tn < kPersistent ? tm * tn : kPersistent;
+    hipLaunchKernelGGL((gemm_block128_tile_kernel<AF, BF, OUT, TA, TB, FAST>), dim3(static_cast<uint32_t>(grid)),
+                       dim3(kThreads), 0, stream, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), a, sa,
+                       b, sb, d, ldd, ep, static_cast<int>(tm), static_cast<int>(tn), vec16_ok(OUT, d, ldd, ep));
     return hipGetLastError();
+}
+
+template <int AF, int BF, int OUT>
+hipError_t launch_out(int64_t M, int64_t N, int64_t K, const uint8_t* a, const ScaleRows& sa, const uint8_t* b,
+                      const ScaleRows& sb, void* d, int64_t ldd, const Epilogue& ep, hipStream_t stream) {
+    // the buffer stores' offsets within a tile's rows are 32-bit
+    const bool fast = ep.beta == 0.0f && vec16_ok(OUT, d, ldd, ep) && N % 8 == 0 && ldd < (int64_t(1) << 21);
+    if (fast) return launch<AF, BF, OUT, 4, 4, true>(M, N, K, a, sa, b, sb, d, ldd, ep, stream);
+    return launch<AF, BF, OUT, 4, 4, false>(M, N, K, a, sa, b, sb, d, ldd, ep, stream);
 }
 
 template <int AF, int BF>
 hipError_t launch_typed(int64_t M, int64_t N, int64_t K, const uint8_t* a, const ScaleRows& sa, const uint8_t* b,
                         const ScaleRows& sb, int out, void* d, int64_t ldd, const Epilogue& ep, hipStream_t stream) {
-    if (out == BSFP8_OUT_BF16)
-        return ep.beta == 0.0f
-                   ? launch<AF, BF, BSFP8_OUT_BF16, true>(M, N, K, a, sa, b, sb, d, ldd, ep, stream)
-                   : launch<AF, BF, BSFP8_OUT_BF16, false>(M, N, K, a, sa, b, sb, d, ldd, ep, stream);
-    return ep.beta == 0.0f ? launch<AF, BF, BSFP8_OUT_F16, true>(M, N, K, a, sa, b, sb, d, ldd, ep, stream)
-                           : launch<AF, BF, BSFP8_OUT_F16, false>(M, N, K, a, sa, b, sb, d, ldd, ep, stream);
+    if (out == BSFP8_OUT_BF16) return launch_out<AF, BF, BSFP8_OUT_BF16>(M, N, K, a, sa, b, sb, d, ldd, ep, stream);
+    return launch_out<AF, BF, BSFP8_OUT_F16>(M, N, K, a, sa, b, sb, d, ldd, ep, stream);
 }
 
 }  // namespace
