@@ -16,7 +16,7 @@ struct ScaleRows {
 template <int FMT>
 constexpr int mfma_fmt() { return FMT == BSFP8_E4M3 ? 0 : 1; }
 
-// 256 x 256 tiles; 16-bit outputs.
+// 256 x 256 tiles.
 hipError_t launch_gemm_block128_big(int64_t M, int64_t N, int64_t K, int a_fmt, const uint8_t* a, const ScaleRows& sa,
                                     int b_fmt, const uint8_t* b, const ScaleRows& sb, int out, void* d, int64_t ldd,
                                     const Epilogue& ep, hipStream_t stream);

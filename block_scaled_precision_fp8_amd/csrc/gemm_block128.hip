@@ -207,7 +207,7 @@ hipError_t launch_gemm_block128(int64_t M, int64_t N, int64_t K, int a_fmt, cons
                                 int b_block_rows, int out, void* d, int64_t ldd, const Epilogue& ep,
                                 hipStream_t stream) {
     const ScaleRows sa = scale_rows(a_scales, M, a_block_rows), sb = scale_rows(b_scales, N, b_block_rows);
-    if (out != BSFP8_OUT_F32 && M > kNarrowMaxM && ((M + 255) / 256) * ((N + 255) / 256) >= kBigTiles)
+    if (M > kNarrowMaxM && ((M + 255) / 256) * ((N + 255) / 256) >= kBigTiles)
         return launch_gemm_block128_big(M, N, K, a_fmt, a, sa, b_fmt, b, sb, out, d, ldd, ep, stream);
     if (a_fmt == BSFP8_E4M3 && b_fmt == BSFP8_E4M3)
         return launch_typed<BSFP8_E4M3, BSFP8_E4M3>(M, N, K, a, sa, b, sb, out, d, ldd, ep, stream);

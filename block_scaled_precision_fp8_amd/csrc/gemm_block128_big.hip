@@ -48,6 +48,20 @@ __device__ __forceinline__ void mfma_scaled(v16f& acc, const u32x8& x, const u32
         : "v"(x), "v"(y), "v"(sx), "v"(sy), "i"(SEL & 1), "i"(SEL >> 1), "i"(CB), "i"(BG));
 }
 
+__device__ __forceinline__ void mfma_bf16_k16(v16f& acc, const u32x4& x, const u32x4& y) {
+    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(x), "v"(y));
+}
+// Two codes (half HI of w) times the scale s -> two bf16, in program order.
+template <int FMT, int HI>
+__device__ __forceinline__ uint32_t widen2(uint32_t w, float s) {
+    uint32_t d;
+    if constexpr (FMT == BSFP8_E4M3)
+        asm volatile("v_cvt_scalef32_pk_bf16_fp8 %0, %1, %2 op_sel:[%3,0,0]" : "=v"(d) : "v"(w), "v"(s), "i"(HI));
+    else
+        asm volatile("v_cvt_scalef32_pk_bf16_bf8 %0, %1, %2 op_sel:[%3,0,0]" : "=v"(d) : "v"(w), "v"(s), "i"(HI));
+    return d;
+}
+
 template <int TA, int TB>
 struct Tile {
     static constexpr int ROWS_A = 64 * TA, ROWS_B = 64 * TB;
@@ -182,8 +196,9 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_block128_tile_kernel(
     };
     clear();
 
+    constexpr bool WIDE = OUT == BSFP8_OUT_F32;
     struct Frag { u32x4 xl[TB], xh[TB], yl[TA], yh[TA]; };
-    Frag fr[2];
+    Frag fr[2];                                      // 16-bit outputs: a step's fragments
     // read piece R (0 .. NR - 1) of step KS of the stage in buffer BUF: B first
     auto read_one = [&](auto R, Frag& dst, auto BUF, auto KS) {
         constexpr int r = R;
@@ -209,6 +224,9 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_block128_tile_kernel(
     // bytes past the last K block (their codes are zero) become a unit scale
     const uint32_t used = (real & 3) ? (1u << (8 * (real & 3))) - 1u : 0xFFFFFFFFu;
     auto take_scales = [&](int group) {
+        // named after the wait for their reads: the compiler takes them as
+        // written when the read is issued
+        name_scales(nxt);
         const uint32_t keep = group == ngr - 1 ? used : 0xFFFFFFFFu;
 #pragma unroll
         for (int t = 0; t < TA + TB; ++t) cur[t] = (nxt[t] & keep) | (0x7F7F7F7Fu & ~keep);
@@ -219,6 +237,38 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_block128_tile_kernel(
 
     constexpr auto C0 = std::integral_constant<int, 0>{};
     constexpr auto C1 = std::integral_constant<int, 1>{};
+
+    // FP32 output: a stage is 8 quarter steps of 16 K.  Half fragments (step ks,
+    // low or high chunk: two quarters' codes) alternate between two sets; the
+    // bf16 operands of a quarter are widened during the MFMAs of the one before.
+    struct Half { u32x4 x[TB], y[TA]; };
+    Half hs[2], wd[2];
+    float fs[TA + TB];                               // the scales of the codes being widened
+    auto read_half = [&](auto R, Half& dst, auto BUF, auto H) {
+        constexpr int r = R, h = H;
+        if constexpr (r < TB) lds_read16<r * 32 * kRowBytes>(dst.x[r], rd_b[BUF][h >> 1][h & 1]);
+        else lds_read16<(r - TB) * 32 * kRowBytes>(dst.y[r - TB], rd_a[BUF][h >> 1][h & 1]);
+    };
+    // piece P (0 .. 4 (TA + TB) - 1) of quarter Q's operands: B and A rows in turn
+    auto widen_one = [&](auto P, auto Q) {
+        constexpr int r = P >> 2, e = P & 3, q = Q;
+        constexpr int both = 2 * (TA < TB ? TA : TB);
+        constexpr bool is_b = r < both ? (r & 1) == 0 : TB > TA;
+        constexpr int t = r < both ? r >> 1 : r - both / 2;
+        constexpr int word = 2 * (q & 1) + (e >> 1);
+        const Half& f = hs[(q >> 1) & 1];
+        Half& w = wd[q & 1];
+        if constexpr (is_b) w.x[t][e] = widen2<BF, e & 1>(f.x[t][word], fs[TA + t]);
+        else w.y[t][e] = widen2<AF, e & 1>(f.y[t][word], fs[t]);
+    };
+    auto take_floats = [&](int byte) {
+#pragma unroll
+        for (int t = 0; t < TA + TB; ++t) {
+            fs[t] = __uint_as_float(((cur[t] >> (8 * byte)) & 255u) << 23);
+            asm volatile("" : "+v"(fs[t]));
+        }
+        asm volatile("s_nop 1");
+    };
 
     int tile = blockIdx.x, tm, tn;
     map_tile(tile, tiles_m, tiles_n, 8, &tm, &tn);
@@ -234,8 +284,17 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_block128_tile_kernel(
     advance();
     asm volatile("s_waitcnt vmcnt(%0)" :: "i"(T::NL) : "memory");
     lds_wait_barrier();
-    static_for<T::NR>([&](auto R) { read_one(R, fr[0], C0, C0); });
     static_for<TA + TB>([&](auto I) { read_scale(I, 0); });
+    if constexpr (!WIDE) {
+        static_for<T::NR>([&](auto R) { read_one(R, fr[0], C0, C0); });
+    } else {
+        static_for<TA + TB>([&](auto R) { read_half(R, hs[0], C0, C0); });
+        static_for<TA + TB>([&](auto R) { read_half(R, hs[1], C0, C1); });
+        lds_wait();
+        take_scales(0);
+        take_floats(0);
+        static_for<4 * (TA + TB)>([&](auto P) { widen_one(P, C0); });
+    }
 
     bool stores = false;                             // an epilogue's stores may be in flight
     for (;;) {
@@ -301,7 +360,78 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_block128_tile_kernel(
             });
             advance();
         };
+        // FP32 output, a stage: quarter q runs its MFMAs, widens quarter q + 1, and
+        //   q = 1, 3  reads half 2, 3 of this stage;
+        //   q = 5     starts with the barrier: every wave has read this stage, and
+        //             the next one has landed (its loads ended five quarters, some
+        //             2500 cycles, ago); then half 0 of the next stage is read, and
+        //             the loads of stage s + 2 go out over the last three quarters;
+        //   q = 7     takes the next stage's scales and reads its half 1.
+        auto run_stage_wide = [&](int s, auto U) {
+            constexpr int u = U;
+            constexpr auto cb = std::integral_constant<int, u & 1>{};
+            constexpr auto nb = std::integral_constant<int, (u & 1) ^ 1>{};
+            const bool group_end = u == 3 || (u == 1 && s + 1 == nst);
+            static_for<8>([&](auto Q_) {
+                constexpr int q = Q_;
+                if constexpr (q & 1) lds_wait();
+                if constexpr (q == 5) {
+                    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                    lds_wait_barrier();
+                    if constexpr (u == 0) {
+                        const bool in = (s >> 2) + 1 < ngr;
+                        scale_dma(in ? m0 : nm0, in ? n0 : nn0, in ? (s >> 2) + 1 : 0, slot ^ 1, 0);
+                        scale_dma(in ? m0 : nm0, in ? n0 : nn0, in ? (s >> 2) + 1 : 0, slot ^ 1, 1);
+                    }
+                    if constexpr (u & 1) {
+                        if (group_end) {
+                            slot ^= 1;
+                            static_for<TA + TB>([&](auto I) { read_scale(I, slot); });
+                        }
+                    }
+                }
+                if constexpr (q == 7) {
+                    if constexpr (u & 1) {
+                        if (group_end) take_scales(s + 1 == nst ? 0 : (s + 1) >> 2);
+                        take_floats(group_end ? 0 : u + 1);
+                    } else {
+                        take_floats(u + 1);
+                    }
+                }
+                static_for<T::NM>([&](auto N_) {
+                    constexpr int n = N_;
+                    constexpr int ti = n / TA, tj = n % TA;
+                    constexpr int W = 4 * (TA + TB) / T::NM;
+                    mfma_bf16_k16(acc[ti][tj], wd[q & 1].x[ti], wd[q & 1].y[tj]);
+                    static_for<W>([&](auto P) {
+                        widen_one(std::integral_constant<int, n * W + P>{}, std::integral_constant<int, (q + 1) & 7>{});
+                    });
+                    if constexpr (q & 1)
+                        static_for<TA + TB>([&](auto R) {
+                            if constexpr (R * T::NM / (TA + TB) == n) {
+                                if constexpr (q == 1) read_half(R, hs[0], cb, std::integral_constant<int, 2>{});
+                                if constexpr (q == 3) read_half(R, hs[1], cb, std::integral_constant<int, 3>{});
+                                if constexpr (q == 5) read_half(R, hs[0], nb, C0);
+                                if constexpr (q == 7) read_half(R, hs[1], nb, C1);
+                            }
+                        });
+                    static_for<T::NL>([&](auto J) {
+                        if constexpr (5 * T::NM + J * 3 * T::NM / T::NL == q * T::NM + n) dma_one(J, cb);
+                    });
+                });
+            });
+            advance();
+        };
         for (int s = 0; s < nst; s += 4) {
+            if constexpr (WIDE) {
+                run_stage_wide(s, C0);
+                run_stage_wide(s + 1, C1);
+                if (s + 2 < nst) {
+                    run_stage_wide(s + 2, std::integral_constant<int, 2>{});
+                    run_stage_wide(s + 3, std::integral_constant<int, 3>{});
+                }
+                continue;
+            }
             run_stage(s, C0);
             run_stage(s + 1, C1);
             if (s + 2 < nst) {
@@ -333,6 +463,7 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_block128_tile_kernel(
         uint8_t* put = strip + (el & 31) * 128;
         const int psw = (el >> 1) & 7, phalf = el >> 5;
         if constexpr (FAST) {
+            static_assert(!WIDE && TB % 2 == 0, "16-bit outputs, column pairs");
             // strips of 32 rows x 64 columns of 16-bit outputs
             const __amdgpu_buffer_rsrc_t rs_d = __builtin_amdgcn_make_buffer_rsrc(
                 static_cast<uint16_t*>(D) + static_cast<int64_t>(m0) * ldd, 0,
@@ -402,10 +533,17 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_block128_tile_kernel(
     // last reads, which have no consumer, are named after the wait so that
     // their registers are not reused while in flight
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    if constexpr (WIDE) {
 #pragma unroll
-    for (int t = 0; t < TB; ++t) asm volatile("" :: "v"(fr[0].xl[t]), "v"(fr[0].xh[t]));
+        for (int t = 0; t < TB; ++t) asm volatile("" :: "v"(hs[0].x[t]), "v"(hs[1].x[t]), "v"(wd[0].x[t]));
 #pragma unroll
-    for (int t = 0; t < TA; ++t) asm volatile("" :: "v"(fr[0].yl[t]), "v"(fr[0].yh[t]));
+        for (int t = 0; t < TA; ++t) asm volatile("" :: "v"(hs[0].y[t]), "v"(hs[1].y[t]), "v"(wd[0].y[t]));
+    } else {
+#pragma unroll
+        for (int t = 0; t < TB; ++t) asm volatile("" :: "v"(fr[0].xl[t]), "v"(fr[0].xh[t]));
+#pragma unroll
+        for (int t = 0; t < TA; ++t) asm volatile("" :: "v"(fr[0].yl[t]), "v"(fr[0].yh[t]));
+    }
     name_scales(nxt);
 }
 
@@ -427,14 +565,17 @@ template <int AF, int BF, int OUT>
 hipError_t launch_out(int64_t M, int64_t N, int64_t K, const uint8_t* a, const ScaleRows& sa, const uint8_t* b,
                       const ScaleRows& sb, void* d, int64_t ldd, const Epilogue& ep, hipStream_t stream) {
     // the buffer stores' offsets within a tile's rows are 32-bit
-    const bool fast = ep.beta == 0.0f && vec16_ok(OUT, d, ldd, ep) && N % 8 == 0 && ldd < (int64_t(1) << 21);
-    if (fast) return launch<AF, BF, OUT, 4, 4, true>(M, N, K, a, sa, b, sb, d, ldd, ep, stream);
+    const bool fast = OUT != BSFP8_OUT_F32 && ep.beta == 0.0f && vec16_ok(OUT, d, ldd, ep) && N % 8 == 0 && ldd < (int64_t(1) << 21);
+    if constexpr (OUT != BSFP8_OUT_F32) {
+        if (fast) return launch<AF, BF, OUT, 4, 4, true>(M, N, K, a, sa, b, sb, d, ldd, ep, stream);
+    }
     return launch<AF, BF, OUT, 4, 4, false>(M, N, K, a, sa, b, sb, d, ldd, ep, stream);
 }
 
 template <int AF, int BF>
 hipError_t launch_typed(int64_t M, int64_t N, int64_t K, const uint8_t* a, const ScaleRows& sa, const uint8_t* b,
                         const ScaleRows& sb, int out, void* d, int64_t ldd, const Epilogue& ep, hipStream_t stream) {
+    if (out == BSFP8_OUT_F32) return launch_out<AF, BF, BSFP8_OUT_F32>(M, N, K, a, sa, b, sb, d, ldd, ep, stream);
     if (out == BSFP8_OUT_BF16) return launch_out<AF, BF, BSFP8_OUT_BF16>(M, N, K, a, sa, b, sb, d, ldd, ep, stream);
     return launch_out<AF, BF, BSFP8_OUT_F16>(M, N, K, a, sa, b, sb, d, ldd, ep, stream);
 }
