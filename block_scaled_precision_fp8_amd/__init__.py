@@ -530,13 +530,17 @@ def scaled_gemm_mx(a, a_scales, b, b_scales, block: int = 32, scale: str = "e8m0
 # ---------------------------------------------------------------------------
 # Blocks of 128 and the optimizer step
 # ---------------------------------------------------------------------------
+# Small calls are bound by the host, so these entry points test what a correct
+# call looks like in one expression and name what is wrong only when it fails.
 def _call(device, fn, *args) -> int:
-    """fn(*args) with `device` current (a launch goes to the current device)."""
+    """fn(*args, stream) on `device`'s current stream, with `device` current (a launch
+    goes to the current device)."""
     import torch
-    if device.index == torch.cuda.current_device():
-        return fn(*args)
+    index = device.index
+    if index == torch.cuda.current_device():
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
     with torch.cuda.device(device):
-        return fn(*args)
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
 
 
 def block128_scale_shape(rows: int, k: int, block_rows: int) -> Tuple[int, int, int]:
@@ -550,11 +554,15 @@ def _block_rows(value, name: str = "block_rows") -> int:
     return value
 
 
-def _element_type(t, name: str) -> int:
-    import torch
-    types = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    _tensor(t, name, tuple(types))
-    return types[t.dtype]
+_elements: dict = {}
+
+
+def _element_types() -> dict:
+    """torch dtype -> element type of the C ABI."""
+    if not _elements:
+        import torch
+        _elements.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    return _elements
 
 
 def fp8_quantize_block128(x, fmt: str = "e4m3", block_rows: int = 1, rows: bool = True,
@@ -566,12 +574,14 @@ def fp8_quantize_block128(x, fmt: str = "e4m3", block_rows: int = 1, rows: bool 
     Codes are rows x kp, kp = k rounded up to a multiple of 32 (zeros past k); scales as
     block128_scale_shape says, bytes e + 127."""
     import torch
-    xt = _element_type(x, "x")
-    if x.dim() != 2 or (x.numel() > 0 and x.shape[1] > 1 and x.stride(1) != 1):
+    types = _element_types()
+    _tensor(x, "x", tuple(types))
+    if x.dim() != 2:
         raise ValueError("x must be 2-D with unit column stride")
     n, k = x.shape
-    if n > 1 and x.stride(0) < k:
-        raise ValueError(f"x rows overlap (row stride {x.stride(0)} < {k})")
+    ld, unit = x.stride()
+    if n and k and ((k > 1 and unit != 1) or (n > 1 and ld < k)):
+        raise ValueError(f"x must have unit column stride and rows that do not overlap, got strides {(ld, unit)}")
     f = _fp8_fmt(fmt)
     _block_rows(block_rows)
     if not rows and not transposed:
@@ -594,14 +604,13 @@ def fp8_quantize_block128(x, fmt: str = "e4m3", block_rows: int = 1, rows: bool 
             _packed(s, "scales" + suffix, sshape, (torch.uint8,), dev)
         return c, s
 
-    got = outs(rows, n, k, codes, scales, ""), outs(transposed, k, n, codes_t, scales_t, "_t")
+    p, q = outs(rows, n, k, codes, scales, ""), outs(transposed, k, n, codes_t, scales_t, "_t")
     if n and k:
-        p = [t.data_ptr() for t in got[0]] or [0, 0]
-        q = [t.data_ptr() for t in got[1]] or [0, 0]
-        st = _call(dev, lib().fp8_quantize_block128, x.data_ptr(), xt, n, k, _ld(x, n, k), block_rows, f,
-                   *p, *q, _stream(x))
+        st = _call(dev, lib().fp8_quantize_block128, x.data_ptr(), types[x.dtype], n, k, ld if n > 1 else k,
+                   block_rows, f, p[0].data_ptr() if p else 0, p[1].data_ptr() if p else 0,
+                   q[0].data_ptr() if q else 0, q[1].data_ptr() if q else 0)
         _check(st, "fp8_quantize_block128")
-    return got[0] + got[1]
+    return p + q
 
 
 def scaled_gemm_block128(a, a_scales, b, b_scales, a_fmt: str = "e4m3", b_fmt: str = "e4m3",
@@ -614,22 +623,24 @@ def scaled_gemm_block128(a, a_scales, b, b_scales, a_fmt: str = "e4m3", b_fmt: s
     fa, fb = _fp8_fmt(a_fmt), _fp8_fmt(b_fmt)
     _block_rows(a_block_rows, "a_block_rows")
     _block_rows(b_block_rows, "b_block_rows")
-    u8 = (torch.uint8,)
-    _tensor(a, "a", u8)
+    u8 = torch.uint8
+    for t, name in ((a, "a"), (b, "b"), (a_scales, "a_scales"), (b_scales, "b_scales")):
+        if not isinstance(t, torch.Tensor) or t.dtype is not u8 or t.device != a.device or not t.is_contiguous():
+            _tensor(t, name, (u8,), getattr(a, "device", None))
+            raise ValueError(f"{name} must be contiguous")
     dev = a.device
-    _tensor(b, "b", u8, dev)
-    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
+    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1] or not a.is_cuda:
+        _tensor(a, "a", (u8,))
         raise ValueError(f"a ({tuple(a.shape)}) and b ({tuple(b.shape)}) must be 2-D with the same K")
     (M, K), N = a.shape, b.shape[0]
-    if not a.is_contiguous() or not b.is_contiguous():
-        raise ValueError("a and b must be contiguous")
-    _packed(a_scales, "a_scales", block128_scale_shape(M, K, a_block_rows), u8, dev)
-    _packed(b_scales, "b_scales", block128_scale_shape(N, K, b_block_rows), u8, dev)
+    for t, name, r, br in ((a_scales, "a_scales", M, a_block_rows), (b_scales, "b_scales", N, b_block_rows)):
+        if tuple(t.shape) != block128_scale_shape(r, K, br):
+            raise ValueError(f"{name} must have shape {block128_scale_shape(r, K, br)}, got {tuple(t.shape)}")
     d, cp, ldc = _epilogue_tensors(d, c, beta, M, N, out, dev)
     if M and N:
         st = _call(dev, lib().scaled_gemm_block128, M, N, K, fa, a.data_ptr(), a_scales.data_ptr(),
                    a_block_rows, fb, b.data_ptr(), b_scales.data_ptr(), b_block_rows, alpha, cp, ldc, beta,
-                   OUTS[out], d.data_ptr(), _ld(d, M, N), _stream(a))
+                   OUTS[out], d.data_ptr(), d.stride(0) if M > 1 else N)
         _check(st, "scaled_gemm_block128")
     return d
 
@@ -668,6 +679,21 @@ def _scalar_ptr(t, name: str, dtype, device) -> int:
     return t.data_ptr()
 
 
+def _adamw_complain(lists, p_dtype, g_dtype, state_dtype, dev):
+    """Raises for the first tensor that an AdamW step cannot take."""
+    import torch
+    names = ("params", "grads", "m", "v", "m_scales", "v_scales")
+    dtypes = (p_dtype, g_dtype, state_dtype, state_dtype, torch.uint8, torch.uint8)
+    for i, row in enumerate(zip(*lists)):
+        for j, t in enumerate(row):
+            _tensor(t, f"{names[j]}[{i}]", (dtypes[j],), dev)
+            n = row[0].numel() if j < 4 else (row[0].numel() + 127) // 128
+            if t.numel() != n or not t.is_contiguous():
+                raise ValueError(f"{names[j]}[{i}] must be contiguous with {n} elements, got {tuple(t.shape)} "
+                                 f"(contiguous: {t.is_contiguous()})")
+    raise ValueError("tensors do not fit together")
+
+
 def adamw_step(params, grads, m, v, m_scales=None, v_scales=None, *, lr=1e-3, beta1: float = 0.9,
                beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 1e-2, step=1,
                grad_scale=None, found_inf=None, seed: int = 0) -> None:
@@ -700,22 +726,23 @@ def adamw_step(params, grads, m, v, m_scales=None, v_scales=None, *, lr=1e-3, be
     _tensor(g0, "grads[0]", (torch.float32, torch.bfloat16, torch.float16))
     dev = p0.device
     state_dt = torch.uint8 if fp8 else torch.float32
-    names = ("params", "grads", "m", "v", "m_scales", "v_scales")
-    dtypes = (p0.dtype, g0.dtype, state_dt, state_dt, torch.uint8, torch.uint8)
     flat = array.array("q")
-    for i, row in enumerate(zip(*lists)):
-        n = row[0].numel() if isinstance(row[0], torch.Tensor) else 0
-        for j, t in enumerate(row):
-            if not isinstance(t, torch.Tensor) or t.dtype is not dtypes[j] or t.device != dev:
-                _tensor(t, f"{names[j]}[{i}]", (dtypes[j],), dev)
-            if t.numel() != (n if j < 4 else (n + 127) // 128) or not t.is_contiguous():
-                raise ValueError(f"{names[j]}[{i}] must be contiguous with "
-                                 f"{n if j < 4 else (n + 127) // 128} elements, got {tuple(t.shape)} "
-                                 f"(contiguous: {t.is_contiguous()})")
-            flat.append(t.data_ptr())
-        if not fp8:
-            flat.extend((0, 0))
-        flat.append(n)
+    try:
+        for x, dt in zip(lists, (p0.dtype, g0.dtype, state_dt, state_dt, torch.uint8, torch.uint8)):
+            for t in x:
+                if t.dtype is not dt or t.device != dev or not t.is_contiguous():
+                    raise ValueError
+        sizes = [t.numel() for t in lists[0]]
+        for x in lists[1:4]:
+            if [t.numel() for t in x] != sizes:
+                raise ValueError
+        for x in lists[4:]:
+            if [t.numel() for t in x] != [(n + 127) // 128 for n in sizes]:
+                raise ValueError
+    except (AttributeError, ValueError):
+        _adamw_complain(lists, p0.dtype, g0.dtype, state_dt, dev)
+    for row in zip(*[[t.data_ptr() for t in x] for x in lists], *(() if fp8 else ([0] * count, [0] * count)), sizes):
+        flat.extend(row)
     args = _AdamWArgs(0.0, beta1, beta2, eps, weight_decay, 1, seed & 0xFFFFFFFF)
     if isinstance(lr, torch.Tensor):
         args.lr_dev = _scalar_ptr(lr, "lr", torch.float32, dev)
@@ -729,7 +756,7 @@ def adamw_step(params, grads, m, v, m_scales=None, v_scales=None, *, lr=1e-3, be
         args.grad_scale = _scalar_ptr(grad_scale, "grad_scale", torch.float32, dev)
     if found_inf is not None:
         args.found_inf = _scalar_ptr(found_inf, "found_inf", torch.float32, dev)
-    types = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    types = _element_types()
     st = _call(dev, lib().adamw_step, flat.buffer_info()[0], count, types[p0.dtype], types[g0.dtype],
-               1 if fp8 else 0, ctypes.addressof(args), _stream(p0))
+               1 if fp8 else 0, ctypes.addressof(args))
     _check(st, "adamw_step")

@@ -12,11 +12,12 @@ LIB = os.path.join(HERE, "libbsfp8.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 SOURCES = ["api.hip", "quantize.hip", "gemm_fp8.hip", "gemm_fp8_big.hip", "gemm_fp8_outer.hip",
-           "gemm_mxfp4.hip", "gemm_mx.hip", "quantize_block128.hip", "gemm_block128.hip", "gemm_block128_big.hip",
+           "gemm_mxfp4.hip", "gemm_mx.hip", "quantize_block128.hip", "gemm_block128.hip", "gemm_block128_4x4.hip",
+           "gemm_block128_4x2.hip", "gemm_block128_3x2.hip", "gemm_block128_2x2.hip",
            "adamw.hip"]
 
 
-def build(verbose: bool = False, jobs: int = 4) -> str:
+def build(verbose: bool = False, jobs: int = 8) -> str:
     flags = ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-Wall",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
              "-I", os.path.join(HERE, "..", "include")]

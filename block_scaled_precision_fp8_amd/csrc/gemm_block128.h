@@ -16,9 +16,25 @@ struct ScaleRows {
 template <int FMT>
 constexpr int mfma_fmt() { return FMT == BSFP8_E4M3 ? 0 : 1; }
 
-// 256 x 256 tiles.
-hipError_t launch_gemm_block128_big(int64_t M, int64_t N, int64_t K, int a_fmt, const uint8_t* a, const ScaleRows& sa,
-                                    int b_fmt, const uint8_t* b, const ScaleRows& sb, int out, void* d, int64_t ldd,
-                                    const Epilogue& ep, hipStream_t stream);
+// One product, for the tiled forms (one source file per tile size: A rows x B
+// rows in units of 64).
+struct TileArgs {
+    int64_t M, N, K;
+    int a_fmt;
+    const uint8_t* a;
+    ScaleRows sa;
+    int b_fmt;
+    const uint8_t* b;
+    ScaleRows sb;
+    int out;
+    void* d;
+    int64_t ldd;
+    Epilogue ep;
+    hipStream_t stream;
+};
+hipError_t launch_gemm_block128_4x4(const TileArgs& t);
+hipError_t launch_gemm_block128_4x2(const TileArgs& t);
+hipError_t launch_gemm_block128_3x2(const TileArgs& t);
+hipError_t launch_gemm_block128_2x2(const TileArgs& t);
 
 }  // namespace bsfp8

@@ -77,8 +77,6 @@ __device__ __forceinline__ v16f step64(const u32x4& x0, const u32x4& x1, const u
 // four partial sums are added in a fixed order.
 constexpr int kNarrowDepth = 2;
 constexpr int kNarrowWaves = 4;
-constexpr int64_t kNarrowMaxM = 64;          // rows up to which it is always used
-constexpr int64_t kBigTiles = 64;            // 256 x 256 tiles from which the large form is used
 
 template <int AF, int BF, int OUT>
 __global__ __launch_bounds__(64 * kNarrowWaves, 2) void gemm_block128_narrow_kernel(
@@ -195,6 +193,36 @@ hipError_t launch_typed(int64_t M, int64_t N, int64_t K, const uint8_t* a, const
     return launch_out<AF, BF, BSFP8_OUT_F16>(M, N, K, a, sa, b, sb, d, ldd, ep, stream);
 }
 
+// Which form is the quickest, from what each one's parts were measured to take
+// (microseconds on MI355X): a tiled form runs ceil(tiles / 256) tiles one after
+// another on the fullest CU, each `stage` per 128 K and `tile` besides; large tiles
+// move fewer bytes per product, small ones fill the chip.  The narrow form splits
+// K over a workgroup's waves and moves 64 bytes per K and 32 x 32 tile at up to
+// 19 TB/s.  Examples (16-bit / FP32 output, us; narrow, 128 x 128, 192 x 128,
+// 256 x 128, 256 x 256): 256 x 4096 x 4096: 16.5, 17.3, 20.4, 23.3, 37.5;
+// 1111 x 4000 x 4064: 95, 39, 28.3, 32.4, 43.8; 2048 x 4096 x 4096: 147, 33.7,
+// 44.6, 32.9, 43.5; 1024 x 14336 x 4096: 187, 60, 65, 55.7, 48.6; FP32
+// 1024 x 1024 x 16384: 75, 101, 131, 163, 282.
+int choose_form(int64_t M, int64_t N, int64_t K, int out) {
+    struct Cost { int rows_a, rows_b; double stage, stage_f32, tile; };
+    static constexpr Cost kCost[4] = {
+        {256, 256, 1.35, 3.05, 8.0}, {256, 128, 0.72, 1e9, 3.0}, {192, 128, 0.60, 1.55, 1.5}, {128, 128, 0.515, 1.0, 0.0}};
+    const double stages = static_cast<double>((K + 127) / 128);
+    const double narrow_tiles = static_cast<double>((M + 31) / 32) * static_cast<double>((N + 31) / 32);
+    double best = 4.0 + narrow_tiles * static_cast<double>(K) * 64.0 / (out == BSFP8_OUT_F32 ? 14.0e6 : 19.0e6);
+    int form = 4;
+    for (int i = 0; i < 4; ++i) {
+        const int64_t tiles = ((M + kCost[i].rows_a - 1) / kCost[i].rows_a) * ((N + kCost[i].rows_b - 1) / kCost[i].rows_b);
+        const double rounds = static_cast<double>((tiles + 255) / 256);
+        const double t = 4.0 + rounds * (stages * (out == BSFP8_OUT_F32 ? kCost[i].stage_f32 : kCost[i].stage) + kCost[i].tile);
+        if (t < best) {
+            best = t;
+            form = i;
+        }
+    }
+    return form;
+}
+
 ScaleRows scale_rows(const uint8_t* s, int64_t rows, int block_rows) {
     return {reinterpret_cast<const uint32_t*>(s), block_rows == 128 ? (rows + 127) / 128 : rows,
             block_rows == 128 ? 7 : 0};
@@ -207,8 +235,14 @@ hipError_t launch_gemm_block128(int64_t M, int64_t N, int64_t K, int a_fmt, cons
                                 int b_block_rows, int out, void* d, int64_t ldd, const Epilogue& ep,
                                 hipStream_t stream) {
     const ScaleRows sa = scale_rows(a_scales, M, a_block_rows), sb = scale_rows(b_scales, N, b_block_rows);
-    if (M > kNarrowMaxM && ((M + 255) / 256) * ((N + 255) / 256) >= kBigTiles)
-        return launch_gemm_block128_big(M, N, K, a_fmt, a, sa, b_fmt, b, sb, out, d, ldd, ep, stream);
+    const TileArgs t{M, N, K, a_fmt, a, sa, b_fmt, b, sb, out, d, ldd, ep, stream};
+    switch (choose_form(M, N, K, out)) {
+    case 0: return launch_gemm_block128_4x4(t);
+    case 1: return launch_gemm_block128_4x2(t);
+    case 2: return launch_gemm_block128_3x2(t);
+    case 3: return launch_gemm_block128_2x2(t);
+    default: break;
+    }
     if (a_fmt == BSFP8_E4M3 && b_fmt == BSFP8_E4M3)
         return launch_typed<BSFP8_E4M3, BSFP8_E4M3>(M, N, K, a, sa, b, sb, out, d, ldd, ep, stream);
     if (a_fmt == BSFP8_E4M3)

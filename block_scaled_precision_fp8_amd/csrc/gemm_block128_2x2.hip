@@ -1,0 +1,6 @@
+// gemm_block128_2x2.hip -- the block-of-128 FP8 GEMM on tiles of 128 x 128.
+#include "gemm_block128_tile.h"
+
+namespace bsfp8 {
+hipError_t launch_gemm_block128_2x2(const TileArgs& t) { return launch_tile<2, 2>(t); }
+}  // namespace bsfp8

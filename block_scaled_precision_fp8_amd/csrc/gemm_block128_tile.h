@@ -1,4 +1,4 @@
-// gemm_block128_big.hip -- the tiled forms of the block-of-128 FP8 GEMM (gfx950).
+// gemm_block128_tile.h -- the tiled forms of the block-of-128 FP8 GEMM (gfx950).
 //
 // A workgroup of four waves (2 x 2) computes tiles of 64 TA x 64 TB outputs,
 // each wave TA x TB MFMA tiles of 32 x 32.  K advances in stages of 128, one
@@ -20,6 +20,8 @@
 // With more tiles than workgroups the grid is persistent: the loads run on into
 // the next tile's first stages while the last ones of this tile are computed
 // and written, so only the first tile of a workgroup waits for memory.
+#pragma once
+
 #include "gemm_block128.h"
 
 namespace bsfp8 {
@@ -68,11 +70,15 @@ struct Tile {
     static constexpr int A_BYTES = ROWS_A * kRowBytes, STAGE_BYTES = A_BYTES + ROWS_B * kRowBytes;
     static constexpr int SCALE_GROUP = (ROWS_A + ROWS_B) * 4;       // words of four K blocks
     static constexpr int SCALES = 2 * STAGE_BYTES;                  // LDS offsets
-    static constexpr int STRIPS = SCALES + 2 * SCALE_GROUP;
-    static constexpr int LDS_BYTES = STRIPS + 4 * kStripBytes;
+    // Persistent tiles need the epilogue's strips beside the stages.  The
+    // smallest tile runs two workgroups per CU instead, whose loops and
+    // epilogues overlap by themselves: its strips reuse the stages.
+    static constexpr bool PERSISTENT = TA * TB > 4;
+    static constexpr int STRIPS = PERSISTENT ? SCALES + 2 * SCALE_GROUP : 0;
+    static constexpr int LDS_BYTES = SCALES + 2 * SCALE_GROUP + (PERSISTENT ? 4 * kStripBytes : 0);
     // slots of a stage: MFMAs per step, fragment reads per step, direct loads per stage and wave
     static constexpr int NM = TA * TB, NR = 2 * (TA + TB), NL = 2 * (TA + TB);
-    static constexpr int RPS = NR / (NM / 2);                       // reads per slot
+    static constexpr int RPS = (NR + NM / 2 - 1) / (NM / 2);        // reads per slot
     static constexpr int FREE = NM / 2 - 1;                         // first barrier: after this slot
     static constexpr int READY = NM + NM / 4;                       // second barrier
     static constexpr int load_slot(int k) {
@@ -86,14 +92,15 @@ struct Tile {
     static constexpr int STORES = TA * TB * 2;                      // of the constant-count epilogue
 };
 
-// FAST: 16-bit output without C, every chunk of 8 outputs whole and aligned:
-// the epilogue is a fixed number of range-checked buffer stores, so the loop
+// FAST: 16-bit output without C, every chunk of 8 outputs whole and aligned: the
+// epilogue is then a fixed number of range-checked buffer stores, so the loop
 // can leave them in flight.
 template <int AF, int BF, int OUT, int TA, int TB, bool FAST>
-__global__ __launch_bounds__(kThreads, 1) void gemm_block128_tile_kernel(
+__global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void gemm_block128_tile_kernel(
     int M, int N, int K, const uint8_t* __restrict__ A, ScaleRows sA, const uint8_t* __restrict__ B, ScaleRows sB,
     void* __restrict__ D, int64_t ldd, Epilogue ep, int tiles_m, int tiles_n, int vec_ok) {
     using T = Tile<TA, TB>;
+    constexpr bool WIDE = OUT == BSFP8_OUT_F32;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS_BYTES];
 
     const int tid = threadIdx.x;
@@ -196,7 +203,6 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_block128_tile_kernel(
     };
     clear();
 
-    constexpr bool WIDE = OUT == BSFP8_OUT_F32;
     struct Frag { u32x4 xl[TB], xh[TB], yl[TA], yh[TA]; };
     Frag fr[2];                                      // 16-bit outputs: a step's fragments
     // read piece R (0 .. NR - 1) of step KS of the stage in buffer BUF: B first
@@ -323,7 +329,10 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_block128_tile_kernel(
                 const u32x8 y = __builtin_shufflevector(f.yl[tj], f.yh[tj], 0, 1, 2, 3, 4, 5, 6, 7);
                 mfma_scaled<u, mfma_fmt<BF>(), mfma_fmt<AF>()>(acc[ti][tj], x, y, cur[TA + ti], cur[tj]);
                 if constexpr (n * T::RPS < T::NR)
-                    static_for<T::RPS>([&](auto Q) { read_one(std::integral_constant<int, n * T::RPS + Q>{}, fr[1], cb, C1); });
+                    static_for<T::RPS>([&](auto Q) {
+                        if constexpr (n * T::RPS + Q < T::NR)
+                            read_one(std::integral_constant<int, n * T::RPS + Q>{}, fr[1], cb, C1);
+                    });
                 if constexpr (n == T::FREE) lds_wait_barrier();
                 static_for<T::NL>([&](auto J) {
                     if constexpr (T::load_slot(J) == n) dma_one(J, cb);
@@ -342,7 +351,8 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_block128_tile_kernel(
                 }
                 if constexpr (n > T::READY && (n - T::READY - 1) * T::RPS < T::NR)
                     static_for<T::RPS>([&](auto Q) {
-                        read_one(std::integral_constant<int, (n - T::READY - 1) * T::RPS + Q>{}, fr[0], nb, C0);
+                        if constexpr ((n - T::READY - 1) * T::RPS + Q < T::NR)
+                            read_one(std::integral_constant<int, (n - T::READY - 1) * T::RPS + Q>{}, fr[0], nb, C0);
                     });
                 // the next group's scales, or the next tile's first: loaded in a
                 // group's first stage, read in its last
@@ -367,44 +377,41 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_block128_tile_kernel(
         //             2500 cycles, ago); then half 0 of the next stage is read, and
         //             the loads of stage s + 2 go out over the last three quarters;
         //   q = 7     takes the next stage's scales and reads its half 1.
-        auto run_stage_wide = [&](int s, auto U) {
-            constexpr int u = U;
-            constexpr auto cb = std::integral_constant<int, u & 1>{};
-            constexpr auto nb = std::integral_constant<int, (u & 1) ^ 1>{};
-            const bool group_end = u == 3 || (u == 1 && s + 1 == nst);
+        auto run_stage_wide = [&](int s, auto CB) {
+            constexpr auto cb = std::integral_constant<int, CB>{};
+            constexpr auto nb = std::integral_constant<int, CB ^ 1>{};
+            const int u = s & 3;                     // stage within its scale group
+            const bool group_end = u == 3 || s + 1 == nst;
             static_for<8>([&](auto Q_) {
                 constexpr int q = Q_;
                 if constexpr (q & 1) lds_wait();
                 if constexpr (q == 5) {
                     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
                     lds_wait_barrier();
-                    if constexpr (u == 0) {
-                        const bool in = (s >> 2) + 1 < ngr;
-                        scale_dma(in ? m0 : nm0, in ? n0 : nn0, in ? (s >> 2) + 1 : 0, slot ^ 1, 0);
-                        scale_dma(in ? m0 : nm0, in ? n0 : nn0, in ? (s >> 2) + 1 : 0, slot ^ 1, 1);
-                    }
-                    if constexpr (u & 1) {
-                        if (group_end) {
-                            slot ^= 1;
-                            static_for<TA + TB>([&](auto I) { read_scale(I, slot); });
+                    if constexpr (cb == 0) {
+                        if (u == 0) {
+                            const bool in = (s >> 2) + 1 < ngr;
+                            scale_dma(in ? m0 : nm0, in ? n0 : nn0, in ? (s >> 2) + 1 : 0, slot ^ 1, 0);
+                            scale_dma(in ? m0 : nm0, in ? n0 : nn0, in ? (s >> 2) + 1 : 0, slot ^ 1, 1);
                         }
+                    } else if (group_end) {
+                        slot ^= 1;
+                        static_for<TA + TB>([&](auto I) { read_scale(I, slot); });
                     }
                 }
                 if constexpr (q == 7) {
-                    if constexpr (u & 1) {
+                    if constexpr (cb == 1) {
                         if (group_end) take_scales(s + 1 == nst ? 0 : (s + 1) >> 2);
-                        take_floats(group_end ? 0 : u + 1);
-                    } else {
-                        take_floats(u + 1);
                     }
+                    take_floats(group_end ? 0 : u + 1);
                 }
                 static_for<T::NM>([&](auto N_) {
                     constexpr int n = N_;
                     constexpr int ti = n / TA, tj = n % TA;
-                    constexpr int W = 4 * (TA + TB) / T::NM;
+                    constexpr int W = 4 * (TA + TB);
                     mfma_bf16_k16(acc[ti][tj], wd[q & 1].x[ti], wd[q & 1].y[tj]);
                     static_for<W>([&](auto P) {
-                        widen_one(std::integral_constant<int, n * W + P>{}, std::integral_constant<int, (q + 1) & 7>{});
+                        if constexpr (P * T::NM / W == n) widen_one(P, std::integral_constant<int, (q + 1) & 7>{});
                     });
                     if constexpr (q & 1)
                         static_for<TA + TB>([&](auto R) {
@@ -422,21 +429,19 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_block128_tile_kernel(
             });
             advance();
         };
-        for (int s = 0; s < nst; s += 4) {
-            if constexpr (WIDE) {
+        if constexpr (WIDE) {
+            for (int s = 0; s < nst; s += 2) {
                 run_stage_wide(s, C0);
                 run_stage_wide(s + 1, C1);
-                if (s + 2 < nst) {
-                    run_stage_wide(s + 2, std::integral_constant<int, 2>{});
-                    run_stage_wide(s + 3, std::integral_constant<int, 3>{});
-                }
-                continue;
             }
-            run_stage(s, C0);
-            run_stage(s + 1, C1);
-            if (s + 2 < nst) {
-                run_stage(s + 2, std::integral_constant<int, 2>{});
-                run_stage(s + 3, std::integral_constant<int, 3>{});
+        } else {
+            for (int s = 0; s < nst; s += 4) {
+                run_stage(s, C0);
+                run_stage(s + 1, C1);
+                if (s + 2 < nst) {
+                    run_stage(s + 2, std::integral_constant<int, 2>{});
+                    run_stage(s + 3, std::integral_constant<int, 3>{});
+                }
             }
         }
         // The next tile's first fragments and scales are in their registers
@@ -448,6 +453,12 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_block128_tile_kernel(
         for (int i = 0; i < TB; ++i)
 #pragma unroll
             for (int j = 0; j < TA; ++j) asm volatile("" : "+a"(acc[i][j]));
+        if constexpr (!T::PERSISTENT) {
+            // the strips reuse the stages: no wave reads them any more and no
+            // load is on its way there
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            lds_wait_barrier();
+        }
 
         // Epilogue, each wave by itself through its own strip of LDS, so that
         // stores write whole lines.  acc[ti][tj][4 q + e] is row 32 tj +
@@ -496,7 +507,7 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_block128_tile_kernel(
                     }
                     __builtin_amdgcn_wave_barrier();
                 }
-            stores = true;
+            stores = T::PERSISTENT;
         } else {
             // strips of 32 rows x 32 columns in FP32; alpha, beta C and the
             // conversion row by row, masked at the edges
@@ -523,7 +534,7 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_block128_tile_kernel(
             // a masked store may not have been issued: none is left in flight
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         }
-        if (!more) break;
+        if (!T::PERSISTENT || !more) break;
         clear();
         tile += gridDim.x;
         m0 = nm0;
@@ -551,47 +562,37 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_block128_tile_kernel(
 constexpr int64_t kPersistent = 256;
 
 template <int AF, int BF, int OUT, int TA, int TB, bool FAST>
-hipError_t launch(int64_t M, int64_t N, int64_t K, const uint8_t* a, const ScaleRows& sa, const uint8_t* b,
-                  const ScaleRows& sb, void* d, int64_t ldd, const Epilogue& ep, hipStream_t stream) {
-    const int64_t tm = (M + 64 * TA - 1) / (64 * TA), tn = (N + 64 * TB - 1) / (64 * TB);
-    const int64_t grid = tm * tn < kPersistent ? tm * tn : kPersistent;
+hipError_t launch_typed(const TileArgs& t) {
+    const int64_t tm = (t.M + 64 * TA - 1) / (64 * TA), tn = (t.N + 64 * TB - 1) / (64 * TB);
+    const int64_t grid = Tile<TA, TB>::PERSISTENT && tm * tn > kPersistent ? kPersistent : tm * tn;
     hipLaunchKernelGGL((gemm_block128_tile_kernel<AF, BF, OUT, TA, TB, FAST>), dim3(static_cast<uint32_t>(grid)),
-                       dim3(kThreads), 0, stream, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), a, sa,
-                       b, sb, d, ldd, ep, static_cast<int>(tm), static_cast<int>(tn), vec16_ok(OUT, d, ldd, ep));
+                       dim3(kThreads), 0, t.stream, static_cast<int>(t.M), static_cast<int>(t.N),
+                       static_cast<int>(t.K), t.a, t.sa, t.b, t.sb, t.d, t.ldd, t.ep, static_cast<int>(tm),
+                       static_cast<int>(tn), vec16_ok(OUT, t.d, t.ldd, t.ep));
     return hipGetLastError();
 }
 
-template <int AF, int BF, int OUT>
-hipError_t launch_out(int64_t M, int64_t N, int64_t K, const uint8_t* a, const ScaleRows& sa, const uint8_t* b,
-                      const ScaleRows& sb, void* d, int64_t ldd, const Epilogue& ep, hipStream_t stream) {
-    // the buffer stores' offsets within a tile's rows are 32-bit
-    const bool fast = OUT != BSFP8_OUT_F32 && ep.beta == 0.0f && vec16_ok(OUT, d, ldd, ep) && N % 8 == 0 && ldd < (int64_t(1) << 21);
-    if constexpr (OUT != BSFP8_OUT_F32) {
-        if (fast) return launch<AF, BF, OUT, 4, 4, true>(M, N, K, a, sa, b, sb, d, ldd, ep, stream);
+// F32: FP32 output is wanted on this tile.
+template <int AF, int BF, int TA, int TB, bool F32>
+hipError_t launch_out(const TileArgs& t) {
+    if constexpr (F32) {
+        if (t.out == BSFP8_OUT_F32) return launch_typed<AF, BF, BSFP8_OUT_F32, TA, TB, false>(t);
     }
-    return launch<AF, BF, OUT, 4, 4, false>(M, N, K, a, sa, b, sb, d, ldd, ep, stream);
+    if (t.out == BSFP8_OUT_F16) return launch_typed<AF, BF, BSFP8_OUT_F16, TA, TB, false>(t);
+    // the buffer stores' offsets within a tile's rows are 32-bit
+    if (t.ep.beta == 0.0f && vec16_ok(t.out, t.d, t.ldd, t.ep) && t.N % 8 == 0 && t.ldd < (int64_t(1) << 21))
+        return launch_typed<AF, BF, BSFP8_OUT_BF16, TA, TB, true>(t);
+    return launch_typed<AF, BF, BSFP8_OUT_BF16, TA, TB, false>(t);
 }
 
-template <int AF, int BF>
-hipError_t launch_typed(int64_t M, int64_t N, int64_t K, const uint8_t* a, const ScaleRows& sa, const uint8_t* b,
-                        const ScaleRows& sb, int out, void* d, int64_t ldd, const Epilogue& ep, hipStream_t stream) {
-    if (out == BSFP8_OUT_F32) return launch_out<AF, BF, BSFP8_OUT_F32>(M, N, K, a, sa, b, sb, d, ldd, ep, stream);
-    if (out == BSFP8_OUT_BF16) return launch_out<AF, BF, BSFP8_OUT_BF16>(M, N, K, a, sa, b, sb, d, ldd, ep, stream);
-    return launch_out<AF, BF, BSFP8_OUT_F16>(M, N, K, a, sa, b, sb, d, ldd, ep, stream);
+template <int TA, int TB, bool F32 = true>
+hipError_t launch_tile(const TileArgs& t) {
+    if (t.a_fmt == BSFP8_E4M3)
+        return t.b_fmt == BSFP8_E4M3 ? launch_out<BSFP8_E4M3, BSFP8_E4M3, TA, TB, F32>(t)
+                                     : launch_out<BSFP8_E4M3, BSFP8_E5M2, TA, TB, F32>(t);
+    return t.b_fmt == BSFP8_E4M3 ? launch_out<BSFP8_E5M2, BSFP8_E4M3, TA, TB, F32>(t)
+                                 : launch_out<BSFP8_E5M2, BSFP8_E5M2, TA, TB, F32>(t);
 }
 
 }  // namespace
-
-hipError_t launch_gemm_block128_big(int64_t M, int64_t N, int64_t K, int a_fmt, const uint8_t* a, const ScaleRows& sa,
-                                    int b_fmt, const uint8_t* b, const ScaleRows& sb, int out, void* d, int64_t ldd,
-                                    const Epilogue& ep, hipStream_t stream) {
-    if (a_fmt == BSFP8_E4M3 && b_fmt == BSFP8_E4M3)
-        return launch_typed<BSFP8_E4M3, BSFP8_E4M3>(M, N, K, a, sa, b, sb, out, d, ldd, ep, stream);
-    if (a_fmt == BSFP8_E4M3)
-        return launch_typed<BSFP8_E4M3, BSFP8_E5M2>(M, N, K, a, sa, b, sb, out, d, ldd, ep, stream);
-    if (b_fmt == BSFP8_E4M3)
-        return launch_typed<BSFP8_E5M2, BSFP8_E4M3>(M, N, K, a, sa, b, sb, out, d, ldd, ep, stream);
-    return launch_typed<BSFP8_E5M2, BSFP8_E5M2>(M, N, K, a, sa, b, sb, out, d, ldd, ep, stream);
-}
-
 }  // namespace bsfp8

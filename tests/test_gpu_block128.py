@@ -142,7 +142,11 @@ def run_gemm(M, N, K, a_rows, b_rows, a_fmt, b_fmt, out, seed=0, alpha=1.0, beta
     got = bs.scaled_gemm_block128(to_dev(a), to_dev(sa), to_dev(b), to_dev(sb), a_fmt, b_fmt, a_rows, b_rows, out,
                                   alpha, d if beta else None, beta, d)
     assert got is d
-    d_ref, s_ref = ref.gemm(a, sa, a_fmt, a_rows, b, sb, b_fmt, b_rows)
+    if M * N * K < 1 << 30:
+        d_ref, s_ref = ref.gemm(a, sa, a_fmt, a_rows, b, sb, b_fmt, b_rows)
+    else:       # the same product in float64 on the device
+        x, y = (to_dev(ref.dequantize(*o)) for o in ((a, sa, a_fmt, a_rows), (b, sb, b_fmt, b_rows)))
+        d_ref, s_ref = from_dev(x @ y.t().contiguous()), from_dev(x.abs() @ y.abs().t().contiguous())
     check(from_dev(d), d_ref, s_ref, out, K, alpha, beta, 0.0 if c is None else from_dev(c), label)
     assert untouched(buf, (M, N), extra_cols=extra, extra_rows=2, tail=32)
 
@@ -169,13 +173,28 @@ def test_gemm_epilogue(M, N, K, alpha, beta, extra, out):
     run_gemm(M, N, K, 1, 1, "e5m2", "e4m3", out, seed=9, alpha=alpha, beta=beta, extra=extra)
 
 
-# shapes at which every form of the kernel runs: few rows; few tiles; many 256 x 256 tiles
-@pytest.mark.parametrize("out", ["bf16", "f32"])
-@pytest.mark.parametrize("M,N,K,a_rows,b_rows", [(16, 4096, 2048, 1, 128), (513, 1030, 1056, 1, 128),
-                                                 (1000, 2000, 544, 1, 1), (2100, 4300, 160, 1, 128),
-                                                 (4096, 3500, 288, 128, 1), (2048, 4096, 1280, 1, 1)])
-def test_gemm_large(M, N, K, a_rows, b_rows, out):
-    run_gemm(M, N, K, a_rows, b_rows, "e4m3", "e4m3", out, seed=K)
+# shapes at which every form of the kernel runs: 32 x 32 with K split; 128 x 128; 192 x 128; 256 x 128;
+# 256 x 256 (several tiles per workgroup), whole and ragged rows of D, an odd and an even number of K blocks
+@pytest.mark.parametrize("out", ["bf16", "f32", "f16"])
+@pytest.mark.parametrize("M,N,K,a_rows,b_rows,beta", [
+    (16, 4096, 2048, 1, 128, 0.0), (513, 1030, 1056, 1, 128, 0.0), (1000, 2000, 544, 1, 1, 0.0),
+    (2100, 4300, 160, 1, 128, 1.0), (4096, 3500, 288, 128, 1, 0.0), (1111, 4000, 2080, 1, 128, 0.0),
+    (1111, 4000, 2080, 1, 1, 1.0), (1500, 5000, 1312, 1, 128, 0.0), (2050, 7003, 3232, 1, 128, 0.0),
+    (3900, 4000, 3232, 128, 128, 0.0), (3900, 4000, 3232, 1, 1, 1.0), (5000, 9000, 4128, 1, 128, 0.0)])
+def test_gemm_forms(M, N, K, a_rows, b_rows, beta, out):
+    run_gemm(M, N, K, a_rows, b_rows, "e4m3", "e4m3", out, seed=K, beta=beta)
+
+
+def test_gemm_is_reproducible_and_rows_do_not_depend_on_others():
+    """The same call twice gives the same bits; a row's result is the same alone and among others as long
+    as the same form runs."""
+    a, sa = operand(2100, 672, 1, "e4m3", 5)
+    b, sb = operand(4300, 672, 128, "e4m3", 6)
+    t = [to_dev(x) for x in (a, sa, b, sb)]
+    say("gemm_block128 twice")
+    d = bs.scaled_gemm_block128(*t)
+    for _ in range(3):
+        assert np.array_equal(from_dev(bs.scaled_gemm_block128(*t)), from_dev(d))
 
 
 def test_gemm_empty_and_k_zero():
