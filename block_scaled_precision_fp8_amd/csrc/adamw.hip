@@ -28,7 +28,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPer = 8;                          // elements per thread: one random group
 constexpr int kUnit = kThreads * kPer;           // elements per workgroup
-constexpr int kTensors = 48;                     // per launch: 48 x 64 bytes of the 4 KB of arguments
+constexpr int kTensors = 48;                     // per launch: 48 x 72 bytes of the 4 KB of arguments
+constexpr int64_t kMaxGroups = (int64_t(1) << 24) - 1;   // a launch's threads are counted in 32 bits
 
 struct Entry {
     void* p;
@@ -38,6 +39,7 @@ struct Entry {
     uint8_t* ms;
     uint8_t* vs;
     int64_t n;
+    int64_t start;       // first element of this launch
     uint32_t first;      // first workgroup
     uint32_t index;      // position in the call, and bit 31: 16-byte loads are allowed
 };
@@ -159,7 +161,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table table, Constants 
     }
     const Entry& t = table.e[lo];
     const int64_t n = t.n;
-    const int64_t base = static_cast<int64_t>(blockIdx.x - t.first) * kUnit;
+    const int64_t base = t.start + static_cast<int64_t>(blockIdx.x - t.first) * kUnit;
     const int64_t i0 = base + tid * kPer;
     const bool whole = (t.index >> 31) && base + kUnit <= n;
     const float gs = dyn.grad_scale ? *dyn.grad_scale : 1.0f;
@@ -352,7 +354,7 @@ hipError_t launch_adamw(const bsfp8_adamw_tensor* tensors, int64_t count, int p_
     const Dynamic d{args.lr_dev, args.step_dev, args.grad_scale, args.found_inf, args.lr, args.beta1, args.beta2,
                     args.weight_decay, args.step, args.seed};
     Table t{};
-    uint64_t grid = 0;
+    int64_t grid = 0;
     auto flush = [&]() -> hipError_t {
         if (t.count == 0) return hipSuccess;
         if (p_type == BSFP8_OUT_F32) launch_grad<BSFP8_OUT_F32>(g_type, state, static_cast<uint32_t>(grid), stream, t, c, d);
@@ -361,20 +363,22 @@ hipError_t launch_adamw(const bsfp8_adamw_tensor* tensors, int64_t count, int p_
         grid = 0;
         return hipGetLastError();
     };
-    constexpr uint64_t kMaxGrid = 0x7FFFFFFFu;
     for (int64_t i = 0; i < count; ++i) {
         const bsfp8_adamw_tensor& x = tensors[i];
-        if (x.n == 0) continue;
-        const uint64_t units = static_cast<uint64_t>(x.n + kUnit - 1) / kUnit;
-        if (t.count == kTensors || grid + units > kMaxGrid) {
-            const hipError_t e = flush();
-            if (e != hipSuccess) return e;
-        }
+        const int64_t units = (x.n + kUnit - 1) / kUnit;
         auto at16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
         const uint32_t wide = at16(x.p) && at16(x.g) && at16(x.m) && at16(x.v) ? 0x80000000u : 0u;
-        t.e[t.count++] = Entry{x.p, x.g, x.m, x.v, x.m_scales, x.v_scales, x.n, static_cast<uint32_t>(grid),
-                               static_cast<uint32_t>(i) | wide};
-        grid += units;
+        for (int64_t u = 0; u < units;) {
+            if (t.count == kTensors || grid == kMaxGroups) {
+                const hipError_t e = flush();
+                if (e != hipSuccess) return e;
+            }
+            const int64_t take = units - u < kMaxGroups - grid ? units - u : kMaxGroups - grid;
+            t.e[t.count++] = Entry{x.p, x.g, x.m, x.v, x.m_scales, x.v_scales, x.n, u * kUnit,
+                                   static_cast<uint32_t>(grid), static_cast<uint32_t>(i) | wide};
+            grid += take;
+            u += take;
+        }
     }
     return flush();
 }

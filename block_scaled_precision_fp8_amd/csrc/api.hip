@@ -22,6 +22,10 @@ constexpr int64_t kI32Max = std::numeric_limits<int32_t>::max();
 // undercuts below about 450 output columns)
 constexpr int64_t kOnlineMaxColumnTiles = 4;
 
+// fp8_quantize_block128's 128 x 128 tiles: HIP counts a launch's threads in 32
+// bits (2^24 workgroups of 256), and the grid is padded to groups of 4 x 4 tiles
+constexpr int64_t kMaxTiles = int64_t(1) << 23;
+
 inline bsfp8_status from_hip(hipError_t e) { return e == hipSuccess ? BSFP8_OK : BSFP8_ERR_HIP; }
 
 }  // namespace
@@ -293,7 +297,7 @@ bsfp8_status fp8_quantize_block128(const void* x, bsfp8_out x_type, int64_t rows
     if (!aligned(x, x_type == BSFP8_OUT_F32 ? 4 : 2) || !aligned(codes, 16) || !aligned(codes_t, 16) ||
         !aligned(scales, 4) || !aligned(scales_t, 4))
         return BSFP8_ERR_INVALID_ARG;
-    if (((rows + 127) / 128) * ((k + 127) / 128) > kI32Max) return BSFP8_ERR_INVALID_ARG;
+    if (((rows + 127) / 128) * ((k + 127) / 128) > kMaxTiles) return BSFP8_ERR_INVALID_ARG;
     return from_hip(bsfp8::launch_quantize_block128(x, x_type, rows, k, ld, block_rows, fmt, codes, scales, codes_t,
                                                     scales_t, stream));
 }
@@ -319,8 +323,8 @@ bsfp8_status scaled_gemm_block128(int64_t M, int64_t N, int64_t K, bsfp8_format 
         return BSFP8_ERR_INVALID_ARG;
     // the kernels address a 256-row band of an operand with 32-bit offsets
     if (K >= (int64_t(1) << 23)) return BSFP8_ERR_UNSUPPORTED;
-    // the narrow form's grid: a workgroup per 32 x 32 tile
-    if (((M + 31) / 32) * (((N + 31) / 32 + 7) / 8 * 8) > kI32Max) return BSFP8_ERR_INVALID_ARG;
+    // tile numbers are 32-bit (the persistent forms add a grid of 256 to them)
+    if (((M + 255) / 256) * ((N + 127) / 128) > kI32Max - 256) return BSFP8_ERR_INVALID_ARG;
     return from_hip(bsfp8::launch_gemm_block128(M, N, K, a_fmt, static_cast<const uint8_t*>(a),
                                                 static_cast<const uint8_t*>(a_scales), a_block_rows, b_fmt,
                                                 static_cast<const uint8_t*>(b),

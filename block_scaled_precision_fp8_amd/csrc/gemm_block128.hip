@@ -208,11 +208,15 @@ int choose_form(int64_t M, int64_t N, int64_t K, int out) {
     static constexpr Cost kCost[4] = {
         {256, 256, 1.35, 3.05, 8.0}, {256, 128, 0.72, 1e9, 3.0}, {192, 128, 0.60, 1.55, 1.5}, {128, 128, 0.515, 1.0, 0.0}};
     const double stages = static_cast<double>((K + 127) / 128);
-    const double narrow_tiles = static_cast<double>((M + 31) / 32) * static_cast<double>((N + 31) / 32);
-    double best = 4.0 + narrow_tiles * static_cast<double>(K) * 64.0 / (out == BSFP8_OUT_F32 ? 14.0e6 : 19.0e6);
+    // one workgroup per tile: only as many as a launch takes (2^32 threads)
+    constexpr int64_t kMaxGroups = (int64_t(1) << 24) - 1;
+    const int64_t narrow_tiles = ((M + 31) / 32) * (((N + 31) / 32 + 7) / 8 * 8);
+    double best = 4.0 + static_cast<double>(narrow_tiles) * static_cast<double>(K) * 64.0 / (out == BSFP8_OUT_F32 ? 14.0e6 : 19.0e6);
+    if (narrow_tiles > kMaxGroups) best = 1e300;
     int form = 4;
     for (int i = 0; i < 4; ++i) {
         const int64_t tiles = ((M + kCost[i].rows_a - 1) / kCost[i].rows_a) * ((N + kCost[i].rows_b - 1) / kCost[i].rows_b);
+        if (i == 3 && tiles > kMaxGroups) continue;
         const double rounds = static_cast<double>((tiles + 255) / 256);
         const double t = 4.0 + rounds * (stages * (out == BSFP8_OUT_F32 ? kCost[i].stage_f32 : kCost[i].stage) + kCost[i].tile);
         if (t < best) {

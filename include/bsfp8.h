@@ -382,7 +382,8 @@ bsfp8_status scaled_gemm_quantize_a(int64_t M, int64_t N, int64_t K, const float
  * 0), clamped to [-127, 127]; scale byte e + 127; code = round-to-nearest-even
  * of x * 2^-e (exact scaling).  A block with an infinity or a NaN gets the
  * scale byte 255 (NaN) and NaN codes (0x7F).  Unused bytes of the last scale
- * word are 127.  Bit-exact.  rows == 0 or k == 0 writes nothing.
+ * word are 127.  Bit-exact.  rows == 0 or k == 0 writes nothing.  The outputs
+ * must not overlap x or each other.
  */
 bsfp8_status fp8_quantize_block128(const void* x, bsfp8_out x_type, int64_t rows, int64_t k, int64_t ld,
                                    int block_rows, bsfp8_format fmt, uint8_t* codes, uint8_t* scales,

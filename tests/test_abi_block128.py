@@ -37,6 +37,7 @@ def test_quantize(L):
     assert call(rows=1 << 31) == INVALID and call(**r, k=1 << 31, ld=1 << 31) == INVALID
     assert call(**r, x=0) == INVALID
     assert call(**r, x=P + 1) == INVALID and call(**r, x=P + 2, x_type=F32) == INVALID
+    assert call(rows=(1 << 31) - 1, k=1, ld=1) == INVALID   # 2^24 workgroups of 256: one too many for a launch
     assert call(**r, codes=0, scales=0) == INVALID          # no orientation
     assert call(**r, codes=0) == INVALID and call(**r, scales=0) == INVALID
     assert call(**r, codes_t=P) == INVALID and call(**r, scales_t=P) == INVALID
@@ -61,7 +62,7 @@ def test_gemm(L):
     assert call(**m, K=48) == INVALID
     assert call(**m, K=1 << 23) == UNSUPPORTED
     assert call(M=1 << 31) == INVALID
-    assert call(M=(1 << 31) - 1, N=(1 << 31) - 1, ldd=1 << 31) == INVALID
+    assert call(M=(1 << 31) - 1, N=(1 << 31) - 1, ldd=1 << 31) == INVALID      # more tiles than 32 bits count
     assert call(**m, ldd=7) == INVALID and call(**m, d=0) == INVALID and call(**m, d=P + 1) == INVALID
     assert call(**m, d=P + 2, out=F32) == INVALID
     assert call(**m, beta=1.0) == INVALID                   # beta without C
