@@ -12,7 +12,8 @@ LIB = os.path.join(HERE, "libbsfp8.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 SOURCES = ["api.hip", "quantize.hip", "gemm_fp8.hip", "gemm_fp8_big.hip", "gemm_fp8_outer.hip",
-           "gemm_mxfp4.hip", "gemm_mx.hip", "quantize_block128.hip", "gemm_block128.hip", "gemm_block128_4x4.hip",
+           "gemm_mxfp4.hip", "gemm_mx.hip", "quantize_block128.hip", "gemm_block128.hip", "gemm_block128_rows.hip",
+           "gemm_block128_4x4.hip",
            "gemm_block128_4x2.hip", "gemm_block128_3x2.hip", "gemm_block128_2x2.hip",
            "adamw.hip"]
 

@@ -23,27 +23,6 @@ namespace {
 using namespace big_tile;
 typedef int v8i __attribute__((ext_vector_type(8)));
 
-// Eight FP8 codes (two dwords) times the scale -> eight bf16 (four dwords),
-// exactly as long as the products are normal bf16.
-template <int FMT>
-__device__ __forceinline__ u32x4 widen8(uint32_t w0, uint32_t w1, float s) {
-    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
-    bf2 a, b, c, d;
-    if constexpr (FMT == BSFP8_E4M3) {
-        a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, false);
-        b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, true);
-        c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, false);
-        d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, true);
-    } else {
-        a = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w0, s, false);
-        b = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w0, s, true);
-        c = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w1, s, false);
-        d = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w1, s, true);
-    }
-    return u32x4{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b),
-                 __builtin_bit_cast(uint32_t, c), __builtin_bit_cast(uint32_t, d)};
-}
-
 // acc += x^T y over 64 K values of one scale block; x: row operand (B, scale
 // byte sb), y: column operand (A, scale byte sa), each lane's 32 codes in two
 // quarters.  All 64 K values share the scales, so the order of K within the
@@ -240,6 +219,7 @@ hipError_t launch_gemm_block128(int64_t M, int64_t N, int64_t K, int a_fmt, cons
                                 hipStream_t stream) {
     const ScaleRows sa = scale_rows(a_scales, M, a_block_rows), sb = scale_rows(b_scales, N, b_block_rows);
     const TileArgs t{M, N, K, a_fmt, a, sa, b_fmt, b, sb, out, d, ldd, ep, stream};
+    if (M <= kRowsMaxM && N <= kRowsMaxN) return launch_gemm_block128_rows(t);
     switch (choose_form(M, N, K, out)) {
     case 0: return launch_gemm_block128_4x4(t);
     case 1: return launch_gemm_block128_4x2(t);

@@ -173,11 +173,11 @@ def test_gemm_epilogue(M, N, K, alpha, beta, extra, out):
     run_gemm(M, N, K, 1, 1, "e5m2", "e4m3", out, seed=9, alpha=alpha, beta=beta, extra=extra)
 
 
-# shapes at which every form of the kernel runs: 32 x 32 with K split; 128 x 128; 192 x 128; 256 x 128;
+# shapes at which every form of the kernel runs: 16 rows; 32 x 32 with K split; 128 x 128; 192 x 128; 256 x 128;
 # 256 x 256 (several tiles per workgroup), whole and ragged rows of D, an odd and an even number of K blocks
 @pytest.mark.parametrize("out", ["bf16", "f32", "f16"])
 @pytest.mark.parametrize("M,N,K,a_rows,b_rows,beta", [
-    (16, 4096, 2048, 1, 128, 0.0), (513, 1030, 1056, 1, 128, 0.0), (1000, 2000, 544, 1, 1, 0.0),
+    (16, 4096, 2048, 1, 128, 0.0), (9, 1001, 9056, 1, 128, 1.0), (16, 6000, 2048, 1, 1, 0.0), (513, 1030, 1056, 1, 128, 0.0), (1000, 2000, 544, 1, 1, 0.0),
     (2100, 4300, 160, 1, 128, 1.0), (4096, 3500, 288, 128, 1, 0.0), (1111, 4000, 2080, 1, 128, 0.0),
     (1111, 4000, 2080, 1, 1, 1.0), (1500, 5000, 1312, 1, 128, 0.0), (2050, 7003, 3232, 1, 128, 0.0),
     (3900, 4000, 3232, 128, 128, 0.0), (3900, 4000, 3232, 1, 1, 1.0), (5000, 9000, 4128, 1, 128, 0.0)])
