@@ -403,8 +403,11 @@ bsfp8_status fp8_quantize_block128(const void* x, bsfp8_out x_type, int64_t rows
  *
  * 16-bit outputs run on the block-scaled FP8 matrix instruction, which takes
  * the E8M0 bytes itself; FP32 output widens the codes, times their scale, to
- * bf16 (exact down to 2^-126) and uses the bf16 instruction.  Accuracy as for
- * scaled_gemm_ex.
+ * bf16 and uses the bf16 instruction (exact for dequantised magnitudes of
+ * 2^-126 and more; smaller ones lose bits, those below 2^-133 count as zero).
+ * Accuracy as for scaled_gemm_ex.  The kernel form is chosen by the sizes and
+ * the output type alone, and no sum depends on timing: equal calls give equal
+ * bits.
  */
 bsfp8_status scaled_gemm_block128(int64_t M, int64_t N, int64_t K, bsfp8_format a_fmt, const void* a,
                                   const void* a_scales, int a_block_rows, bsfp8_format b_fmt, const void* b,

@@ -41,21 +41,24 @@ def unwords(w: np.ndarray, nkb: int) -> np.ndarray:
 def quantize(x: np.ndarray, fmt: str, block_rows: int):
     """Codes rows x up(k, 32) and scale words of a float32 matrix."""
     rows, k = x.shape
-    nkb, R = up(k, 128) // 128, up(rows, block_rows) // block_rows
+    x = x.astype(np.float64)
+    bad = ~np.isfinite(x)
+    edges_r, edges_k = np.arange(0, rows, block_rows), np.arange(0, k, 128)
+
+    def per_block(f, v):
+        return f.reduceat(f.reduceat(v, edges_r, 0), edges_k, 1)
+
+    def spread(v):
+        return np.repeat(np.repeat(v, block_rows, 0)[:rows], 128, 1)[:, :k]
+
+    e = exponent(per_block(np.maximum, np.abs(np.where(bad, 0.0, x))), fmt)
+    nan = per_block(np.logical_or, bad)
     codes = np.zeros((rows, up(k, 32)), dtype=np.uint8)
-    scales = np.zeros((R, nkb), dtype=np.uint8)
-    for i in range(R):
-        for j in range(nkb):
-            r, c = slice(i * block_rows, min((i + 1) * block_rows, rows)), slice(128 * j, min(128 * j + 128, k))
-            b = x[r, c].astype(np.float64)
-            if not np.all(np.isfinite(b)):
-                scales[i, j] = 255
-                codes[r, 128 * j:128 * j + 128] = 0x7F
-                continue
-            e = int(exponent(np.abs(b).max(), fmt))
-            scales[i, j] = e + 127
-            codes[r, c] = encode(fmt, np.ldexp(b, -e)).reshape(b.shape)
-    return codes, words(scales)
+    codes[:, :k] = encode(fmt, np.ldexp(np.where(bad, 0.0, x), -spread(e))).reshape(rows, k)
+    # a block with an infinity or a NaN: NaN scale, NaN codes (its padding columns too)
+    wide = np.repeat(np.repeat(nan, block_rows, 0)[:rows], 128, 1)[:, :codes.shape[1]]
+    codes[wide] = 0x7F
+    return codes, words(np.where(nan, 255, e + 127).astype(np.uint8))
 
 
 def scale_values(bytes_: np.ndarray) -> np.ndarray:

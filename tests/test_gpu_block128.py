@@ -38,7 +38,7 @@ def values(rows, k, dtype, seed):
 
 # ------------------------------------------------------------------ quantiser
 SHAPES = [(1, 1), (1, 128), (3, 40), (16, 512), (128, 128), (129, 127), (130, 257), (64, 1000), (257, 640),
-          (1, 8192), (33, 2049)]
+          (1, 8192), (33, 2049), (600, 700), (513, 130), (130, 1300)]
 
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
@@ -100,9 +100,10 @@ def test_quantize_special_values():
             xf = x.numpy()
             codes, scales = ref.quantize(xf, fmt, block_rows)
             codes_t, scales_t = ref.quantize(np.ascontiguousarray(xf.T), fmt, block_rows)
-            # a non-finite block's padding columns may hold NaN codes too
-            assert np.array_equal(got[0][:, :300], codes[:, :300]) and np.array_equal(got[1], scales)
-            assert np.array_equal(got[2][:, :200], codes_t[:, :200]) and np.array_equal(got[3], scales_t)
+            for a, b in zip(got, (codes, scales, codes_t, scales_t)):
+                assert np.array_equal(a, b)
+            rows_only = [from_dev(t) for t in bs.fp8_quantize_block128(x.cuda(), fmt, block_rows)]
+            assert np.array_equal(rows_only[0], codes) and np.array_equal(rows_only[1], scales)
 
 
 # ------------------------------------------------------------------ GEMM
@@ -234,6 +235,46 @@ def test_gemm_nan_scale_and_unused_scale_bytes(M, N, K, out):
         check(d[keep], d_ref[keep], s_ref[keep], out, k, label="other rows")
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(5, 40, 700), (64, 100, 300), (300, 300, 1000), (2100, 4300, 300)])
+def test_gemm_carries_non_finite_inputs(M, N, K, out):
+    """An infinity in x makes its row of x w^T NaN and leaves the others; NaN codes do the same."""
+    import torch
+    x, w = values(M, K, torch.float32, 1), values(N, K, torch.float32, 2)
+    x[M // 2, 200] = float("inf")
+    say(f"gemm_block128 non-finite {M}x{N}x{K} {out}")
+    xq, xs = bs.fp8_quantize_block128(x.cuda(), "e4m3", 1)
+    wq, ws = bs.fp8_quantize_block128(w.cuda(), "e4m3", 128)
+    d = from_dev(bs.scaled_gemm_block128(xq, xs, wq, ws, out=out))
+    keep = np.arange(M) != M // 2
+    assert np.isnan(d[M // 2]).all() and np.isfinite(d[keep]).all()
+    xs.clamp_(max=200)          # the scale byte no longer says NaN: the codes still do
+    d = from_dev(bs.scaled_gemm_block128(xq, xs, wq, ws, out=out))
+    assert np.isnan(d[M // 2]).all() and np.isfinite(d[keep]).all()
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", [(7, 120, 256), (50, 120, 256), (300, 264, 256), (2100, 4304, 160)])
+def test_gemm_output_at_an_odd_address(M, N, K, out):
+    """D one element into a buffer, with an odd row stride: no 16-byte stores."""
+    import torch
+    a, sa = operand(M, K, 1, "e4m3", 5)
+    b, sb = operand(N, K, 128, "e4m3", 6)
+    if out == "f16":
+        sa = sa - 20
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[out]
+    buf, view = guarded((M, N + 1), dt, extra_cols=2, extra_rows=1, tail=16)
+    before = buf.clone()
+    say(f"gemm_block128 odd address {M}x{N}x{K} {out}")
+    t = [to_dev(v) for v in (a, sa, b, sb)]
+    bs.scaled_gemm_block128(*t, out=out, d=view[:, 1:])
+    assert torch.equal(view[:, 1:], bs.scaled_gemm_block128(*t, out=out))
+    view[:, 1:] = 0
+    grid, want = buf.view(torch.uint8), before
+    want[: M * (N + 3)].view(M, N + 3)[:, 1:N + 1] = 0
+    assert torch.equal(grid, want.view(torch.uint8))
+
+
 def test_gemm_extreme_scales():
     """Scale bytes at both ends: products are FP32 values as long as they are normal there."""
     import torch
@@ -278,6 +319,22 @@ def test_layer_products_from_quantised_operands():
 
 
 # ------------------------------------------------------------------ streams and graphs
+def test_two_streams_at_once():
+    """Independent calls on two streams, no shared state between them."""
+    import torch
+    say("block128 on two streams")
+    w, ws = bs.fp8_quantize_block128(values(3000, 2048, torch.float32, 1).cuda(), "e4m3", 128)
+    xs = [values(m, 2048, torch.bfloat16, m).cuda() for m in (16, 700, 1800, 2100)]
+    want = [bs.scaled_gemm_block128(*bs.fp8_quantize_block128(x), w, ws) for x in xs]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for i in range(24):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(bs.scaled_gemm_block128(*bs.fp8_quantize_block128(xs[i % 4]), w, ws))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i % 4]) for i, g in enumerate(got))
+
+
 def test_stream_and_graph():
     import torch
     M, N, K = 48, 300, 400
