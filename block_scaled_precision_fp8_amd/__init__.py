@@ -624,19 +624,24 @@ def scaled_gemm_block128(a, a_scales, b, b_scales, a_fmt: str = "e4m3", b_fmt: s
     _block_rows(a_block_rows, "a_block_rows")
     _block_rows(b_block_rows, "b_block_rows")
     u8 = torch.uint8
-    for t, name in ((a, "a"), (b, "b"), (a_scales, "a_scales"), (b_scales, "b_scales")):
-        if not isinstance(t, torch.Tensor) or t.dtype is not u8 or t.device != a.device or not t.is_contiguous():
-            _tensor(t, name, (u8,), getattr(a, "device", None))
-            raise ValueError(f"{name} must be contiguous")
+    _tensor(a, "a", (u8,))
     dev = a.device
-    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1] or not a.is_cuda:
-        _tensor(a, "a", (u8,))
+    index = dev.index
+    for t, name in ((a, "a"), (b, "b"), (a_scales, "a_scales"), (b_scales, "b_scales")):
+        if not isinstance(t, torch.Tensor) or t.dtype is not u8 or t.get_device() != index or not t.is_contiguous():
+            _tensor(t, name, (u8,), dev)
+            raise ValueError(f"{name} must be contiguous")
+    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
         raise ValueError(f"a ({tuple(a.shape)}) and b ({tuple(b.shape)}) must be 2-D with the same K")
     (M, K), N = a.shape, b.shape[0]
     for t, name, r, br in ((a_scales, "a_scales", M, a_block_rows), (b_scales, "b_scales", N, b_block_rows)):
         if tuple(t.shape) != block128_scale_shape(r, K, br):
             raise ValueError(f"{name} must have shape {block128_scale_shape(r, K, br)}, got {tuple(t.shape)}")
-    d, cp, ldc = _epilogue_tensors(d, c, beta, M, N, out, dev)
+    if d is None and c is None and beta == 0.0:
+        _key(OUTS, out, "output type")
+        d, cp, ldc = torch.empty((M, N), dtype=getattr(torch, _OUT_DTYPES[out]), device=dev), 0, 0
+    else:
+        d, cp, ldc = _epilogue_tensors(d, c, beta, M, N, out, dev)
     if M and N:
         st = _call(dev, lib().scaled_gemm_block128, M, N, K, fa, a.data_ptr(), a_scales.data_ptr(),
                    a_block_rows, fb, b.data_ptr(), b_scales.data_ptr(), b_block_rows, alpha, cp, ldc, beta,
@@ -725,12 +730,13 @@ def adamw_step(params, grads, m, v, m_scales=None, v_scales=None, *, lr=1e-3, be
     _tensor(p0, "params[0]", (torch.float32, torch.bfloat16))
     _tensor(g0, "grads[0]", (torch.float32, torch.bfloat16, torch.float16))
     dev = p0.device
+    index = dev.index
     state_dt = torch.uint8 if fp8 else torch.float32
     flat = array.array("q")
     try:
         for x, dt in zip(lists, (p0.dtype, g0.dtype, state_dt, state_dt, torch.uint8, torch.uint8)):
             for t in x:
-                if t.dtype is not dt or t.device != dev or not t.is_contiguous():
+                if t.dtype is not dt or t.get_device() != index or not t.is_contiguous():
                     raise ValueError
         sizes = [t.numel() for t in lists[0]]
         for x in lists[1:4]:

@@ -64,6 +64,13 @@ __device__ __forceinline__ uint32_t widen2(uint32_t w, float s) {
     return d;
 }
 
+// Two FP32 values -> two bf16, round to nearest even, in one instruction.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, b2));
+}
+
 template <int TA, int TB>
 struct Tile {
     static constexpr int ROWS_A = 64 * TA, ROWS_B = 64 * TB;
@@ -92,7 +99,7 @@ struct Tile {
     static constexpr int STORES = TA * TB * 2;                      // of the constant-count epilogue
 };
 
-// FAST: 16-bit output without C, every chunk of 8 outputs whole and aligned: the
+// FAST: bf16 output, alpha = 1, without C, every chunk of 8 outputs whole and aligned: the
 // epilogue is then a fixed number of range-checked buffer stores, so the loop
 // can leave them in flight.
 template <int AF, int BF, int OUT, int TA, int TB, bool FAST>
@@ -474,11 +481,20 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
         uint8_t* put = strip + (el & 31) * 128;
         const int psw = (el >> 1) & 7, phalf = el >> 5;
         if constexpr (FAST) {
-            static_assert(!WIDE && TB % 2 == 0, "16-bit outputs, column pairs");
+            static_assert(OUT == BSFP8_OUT_BF16 && TB % 2 == 0, "bf16 output, column pairs");
             // strips of 32 rows x 64 columns of 16-bit outputs
             const __amdgpu_buffer_rsrc_t rs_d = __builtin_amdgcn_make_buffer_rsrc(
                 static_cast<uint16_t*>(D) + static_cast<int64_t>(m0) * ldd, 0,
                 min(T::ROWS_A, M - m0) * static_cast<int>(ldd) * 2, 0x00020000);
+            // byte offset of this lane's first chunk of each column pair; past
+            // column N one that stays out of range whatever rows are added
+            const uint32_t ld2 = static_cast<uint32_t>(ldd) * 2;
+            uint32_t at[TB / 2];
+#pragma unroll
+            for (int tp = 0; tp < TB / 2; ++tp) {
+                const int col = nw + 64 * tp + 8 * schunk;
+                at[tp] = col < N ? (wm * 32 * TA + srow) * ld2 + col * 2 : 0x80000000u;
+            }
 #pragma unroll
             for (int tj = 0; tj < TA; ++tj)
 #pragma unroll
@@ -488,22 +504,15 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const v16f& a = acc[2 * tp + t][tj];
-                            const uint32_t h0 = to_half_bits<OUT>(ep.alpha * a[4 * q + 0]);
-                            const uint32_t h1 = to_half_bits<OUT>(ep.alpha * a[4 * q + 1]);
-                            const uint32_t h2 = to_half_bits<OUT>(ep.alpha * a[4 * q + 2]);
-                            const uint32_t h3 = to_half_bits<OUT>(ep.alpha * a[4 * q + 3]);
                             *reinterpret_cast<uint2*>(put + (((4 * t + q) ^ psw) << 4) + 8 * phalf) =
-                                make_uint2(h0 | (h1 << 16), h2 | (h3 << 16));
+                                make_uint2(bf16_pair(a[4 * q + 0], a[4 * q + 1]), bf16_pair(a[4 * q + 2], a[4 * q + 3]));
                         }
                     __builtin_amdgcn_wave_barrier();
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int R = 8 * i + srow;
                         const u32x4 w = *reinterpret_cast<const u32x4*>(strip + R * 128 + ((schunk ^ ((R >> 1) & 7)) << 4));
-                        const int col = nw + 64 * tp + 8 * schunk;
-                        const uint32_t off = col < N ? static_cast<uint32_t>(((mw - m0 + 32 * tj + R) * static_cast<int>(ldd) + col) * 2)
-                                                     : 0x80000000u;
-                        __builtin_amdgcn_raw_buffer_store_b128(w, rs_d, off, 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b128(w, rs_d, at[tp] + (32 * tj + 8 * i) * ld2, 0, 0);
                     }
                     __builtin_amdgcn_wave_barrier();
                 }
@@ -580,7 +589,7 @@ hipError_t launch_out(const TileArgs& t) {
     }
     if (t.out == BSFP8_OUT_F16) return launch_typed<AF, BF, BSFP8_OUT_F16, TA, TB, false>(t);
     // the buffer stores' offsets within a tile's rows are 32-bit
-    if (t.ep.beta == 0.0f && vec16_ok(t.out, t.d, t.ldd, t.ep) && t.N % 8 == 0 && t.ldd < (int64_t(1) << 21))
+    if (t.ep.alpha == 1.0f && t.ep.beta == 0.0f && vec16_ok(t.out, t.d, t.ldd, t.ep) && t.N % 8 == 0 && t.ldd < (int64_t(1) << 21))
         return launch_typed<AF, BF, BSFP8_OUT_BF16, TA, TB, true>(t);
     return launch_typed<AF, BF, BSFP8_OUT_BF16, TA, TB, false>(t);
 }
