@@ -635,7 +635,7 @@ def scaled_gemm_block128(a, a_scales, b, b_scales, a_fmt: str = "e4m3", b_fmt: s
         raise ValueError(f"a ({tuple(a.shape)}) and b ({tuple(b.shape)}) must be 2-D with the same K")
     (M, K), N = a.shape, b.shape[0]
     for t, name, r, br in ((a_scales, "a_scales", M, a_block_rows), (b_scales, "b_scales", N, b_block_rows)):
-        if tuple(t.shape) != block128_scale_shape(r, K, br):
+        if t.shape != ((K + 511) // 512, (r + br - 1) // br, 4):
             raise ValueError(f"{name} must have shape {block128_scale_shape(r, K, br)}, got {tuple(t.shape)}")
     if d is None and c is None and beta == 0.0:
         _key(OUTS, out, "output type")

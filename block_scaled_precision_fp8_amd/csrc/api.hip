@@ -311,7 +311,8 @@ bsfp8_status scaled_gemm_block128(int64_t M, int64_t N, int64_t K, bsfp8_format 
     if ((a_block_rows != 1 && a_block_rows != 128) || (b_block_rows != 1 && b_block_rows != 128))
         return BSFP8_ERR_UNSUPPORTED;
     if (M < 0 || N < 0 || K < 0 || (K % 32) != 0) return BSFP8_ERR_INVALID_ARG;
-    if (M > kI32Max || N > kI32Max || K > kI32Max) return BSFP8_ERR_INVALID_ARG;
+    // row and column numbers run past the last tile's edge in 32 bits
+    if (M > kI32Max - 256 || N > kI32Max - 256 || K > kI32Max) return BSFP8_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return BSFP8_OK;
     const uintptr_t es = out == BSFP8_OUT_F32 ? 4 : 2;
     if (!d || ldd < N || !aligned(d, es)) return BSFP8_ERR_INVALID_ARG;

@@ -371,7 +371,7 @@ bsfp8_status scaled_gemm_quantize_a(int64_t M, int64_t N, int64_t K, const float
  *         BSFP8_OUT_F16), row-major, leading dimension ld >= k, aligned to its
  *         element size.  16-byte aligned x with a row stride of a multiple of
  *         16 bytes is read with 16-byte loads; anything else element by element.
- * rows, k: >= 0, any value, at most 2^31 - 1.
+ * rows, k: >= 0, any value, at most 2^31 - 1 and 2^23 tiles of 128 x 128.
  * block_rows: 1 (1 x 128 blocks) or 128 (128 x 128 blocks); for the transpose
  *         the blocks are those of x^T.
  * codes, scales:     out, the codes and scales of x; both NULL: not wanted.
@@ -395,8 +395,8 @@ bsfp8_status fp8_quantize_block128(const void* x, bsfp8_out x_type, int64_t rows
  *
  * a: M x K codes, a_scales E8M0 words [ceil(K / 512)][M or ceil(M / 128)][4]
  * for a_block_rows 1 or 128; b: N x K codes (the K x N column-major operand)
- * likewise.  a and b 16-byte aligned, the scales 4-byte aligned.  All formats
- * (E4M3, E5M2) and block shapes mix.  K a multiple of 32, below 2^23 (the
+ * likewise.  a and b 16-byte aligned, the scales 4-byte aligned.  M and N at
+ * most 2^31 - 257.  All formats (E4M3, E5M2) and block shapes mix.  K a multiple of 32, below 2^23 (the
  * kernels address a 256-row band of an operand with 32-bit offsets; larger K
  * returns BSFP8_ERR_UNSUPPORTED).  alpha, c, ldc, beta, out, d, ldd: as for
  * scaled_gemm_ex.  A NaN scale makes every output that uses its block NaN.

@@ -62,7 +62,8 @@ def test_gemm(L):
     assert call(**m, K=48) == INVALID
     assert call(**m, K=1 << 23) == UNSUPPORTED
     assert call(M=1 << 31) == INVALID
-    assert call(M=(1 << 31) - 1, N=(1 << 31) - 1, ldd=1 << 31) == INVALID      # more tiles than 32 bits count
+    assert call(M=(1 << 31) - 256) == INVALID and call(M=8, N=(1 << 31) - 256, ldd=1 << 31) == INVALID
+    assert call(M=(1 << 31) - 512, N=(1 << 31) - 512, ldd=1 << 31) == INVALID  # more tiles than 32 bits count
     assert call(**m, ldd=7) == INVALID and call(**m, d=0) == INVALID and call(**m, d=P + 1) == INVALID
     assert call(**m, d=P + 2, out=F32) == INVALID
     assert call(**m, beta=1.0) == INVALID                   # beta without C
