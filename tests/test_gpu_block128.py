@@ -291,6 +291,27 @@ def test_gemm_extreme_scales():
             check(d, d_ref, s_ref, out, 256, label="extreme")
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("M,N,K", [(9, 50, 256), (40, 50, 256), (300, 264, 544), (2100, 4304, 160)])
+def test_gemm_smallest_scale(M, N, K, fmt, out):
+    """Scale byte 0 (2^-127) on either side, codes of 2 and more: dequantised magnitudes are 2^-126 and more."""
+    a, sa = operand(M, K, 1, fmt, 1)
+    b, sb = operand(N, K, 128, fmt, 2)
+    two = 0x40
+    a, b = a | two, b | two
+    for pa, pb in ((0, 230), (230, 0)):
+        # E4M3: | 0x40 could make the NaN code 0x7F
+        x, y = (np.where((t & 0x7F) >= (0x7F if fmt == "e4m3" else 0x7C), 0x41, t).astype(np.uint8) for t in (a, b))
+        sa[:], sb[:] = pa, pb
+        label = f"gemm_block128 {M}x{N}x{K} {fmt} scales {pa},{pb} {out}"
+        say(label)
+        d = bs.scaled_gemm_block128(to_dev(x), to_dev(sa), to_dev(y), to_dev(sb), fmt, fmt, 1, 128, out)
+        u, v = to_dev(ref.dequantize(x, sa, fmt, 1)), to_dev(ref.dequantize(y, sb, fmt, 128))
+        d_ref, s_ref = from_dev(u @ v.t().contiguous()), from_dev(u.abs() @ v.abs().t().contiguous())
+        check(from_dev(d), d_ref, s_ref, out, K, label=label)
+
+
 # ------------------------------------------------------------------ a linear layer's three products
 def test_layer_products_from_quantised_operands():
     """y = x w^T, dx = g w, dw = g^T x from the quantiser's outputs, against float64 products of the
