@@ -348,11 +348,11 @@ bsfp8_status adamw_step(const bsfp8_adamw_tensor* tensors, int64_t count, bsfp8_
         return BSFP8_ERR_INVALID_ARG;
     const bool fp8 = state == BSFP8_STATE_FP8;
     const int64_t ps = p_type == BSFP8_OUT_F32 ? 4 : 2, gs = g_type == BSFP8_OUT_F32 ? 4 : 2, ss = fp8 ? 1 : 4;
-    // byte ranges that are written, and those that are only read (the gradients)
+    // byte ranges that are written, and those that are only read (gradients, device scalars)
     struct Range { uintptr_t at, end; bool written; };
     std::vector<Range> ranges;
     try {
-        ranges.reserve(static_cast<size_t>(count) * 6);
+        ranges.reserve(static_cast<size_t>(count) * 6 + 4);
         for (int64_t i = 0; i < count; ++i) {
             const bsfp8_adamw_tensor& t = tensors[i];
             if (t.n < 0 || t.n > (int64_t(1) << 40)) return BSFP8_ERR_INVALID_ARG;
@@ -372,6 +372,17 @@ bsfp8_status adamw_step(const bsfp8_adamw_tensor* tensors, int64_t count, bsfp8_
                 add(t.m_scales, (t.n + 127) / 128, true);
                 add(t.v_scales, (t.n + 127) / 128, true);
             }
+        }
+        if (!ranges.empty()) {
+            // read by every workgroup, while others already write
+            auto scalar = [&](const void* p, uintptr_t bytes) {
+                const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+                if (p) ranges.push_back({a, a + bytes, false});
+            };
+            scalar(args->lr_dev, 4);
+            scalar(args->step_dev, 8);
+            scalar(args->grad_scale, 4);
+            scalar(args->found_inf, 4);
         }
         std::sort(ranges.begin(), ranges.end(), [](const Range& x, const Range& y) { return x.at < y.at; });
     } catch (const std::bad_alloc&) {

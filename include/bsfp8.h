@@ -396,9 +396,9 @@ bsfp8_status fp8_quantize_block128(const void* x, bsfp8_out x_type, int64_t rows
  * a: M x K codes, a_scales E8M0 words [ceil(K / 512)][M or ceil(M / 128)][4]
  * for a_block_rows 1 or 128; b: N x K codes (the K x N column-major operand)
  * likewise.  a and b 16-byte aligned, the scales 4-byte aligned.  M and N at
- * most 2^31 - 257.  All formats (E4M3, E5M2) and block shapes mix.  K a multiple of 32, below 2^23 (the
- * kernels address a 256-row band of an operand with 32-bit offsets; larger K
- * returns BSFP8_ERR_UNSUPPORTED).  alpha, c, ldc, beta, out, d, ldd: as for
+ * most 2^31 - 257.  All formats (E4M3, E5M2) and block shapes mix.  K a
+ * multiple of 32, below 2^23 (the kernels address a 256-row band of an operand
+ * with 32-bit offsets; larger K returns BSFP8_ERR_UNSUPPORTED).  alpha, c, ldc, beta, out, d, ldd: as for
  * scaled_gemm_ex.  A NaN scale makes every output that uses its block NaN.
  *
  * 16-bit outputs run on the block-scaled FP8 matrix instruction, which takes
@@ -443,7 +443,7 @@ typedef struct {
     int64_t step;               /* the number of this step, >= 1 */
     uint32_t seed;              /* of the stochastic rounding */
     const float* lr_dev;        /* replaces lr */
-    const int64_t* step_dev;    /* replaces step */
+    const int64_t* step_dev;    /* replaces step, >= 1 when the kernel runs */
     const float* grad_scale;    /* multiplies every gradient */
     const float* found_inf;     /* not zero: the step changes nothing */
 } bsfp8_adamw_args;
@@ -472,8 +472,8 @@ typedef struct {
  * Zeroed codes and scale bytes are valid initial states, as zeroed FP32 ones.
  *
  * beta1, beta2 in [0, 1); eps >= 0; all finite.  The p, m, v and scale arrays
- * of a call must not overlap each other or the gradients
- * (BSFP8_ERR_INVALID_ARG).  Infinities and NaN in gradients spread to p, m and
+ * of a call must not overlap each other, the gradients or the scalars that args
+ * points to (BSFP8_ERR_INVALID_ARG).  Infinities and NaN in gradients spread to p, m and
  * v; with FP8 states to the whole block of 128 (scale byte 255): use found_inf.
  */
 bsfp8_status adamw_step(const bsfp8_adamw_tensor* tensors, int64_t count, bsfp8_out p_type, bsfp8_out g_type,

@@ -112,6 +112,9 @@ def test_adamw(L):
     assert call(tensors(n, n)) == INVALID
     assert call(tensors({**n, "ms": P + 0x20010, "vs": P + 0x50000}), state=1) == INVALID
     assert call(tensors({**n, "p": P + 0x20000})) == INVALID
+    # device scalars inside what the step writes
+    for k, at in (("lr_dev", P + 396), ("step_dev", P + 0x20000), ("grad_scale", P + 0x30000 + 8), ("found_inf", P)):
+        assert call(tensors(n), **{k: at}) == INVALID, k
 
 
 def test_binding_refusals():
