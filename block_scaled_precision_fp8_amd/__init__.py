@@ -766,3 +766,6 @@ def adamw_step(params, grads, m, v, m_scales=None, v_scales=None, *, lr=1e-3, be
     st = _call(dev, lib().adamw_step, flat.buffer_info()[0], count, types[p0.dtype], types[g0.dtype],
                1 if fp8 else 0, ctypes.addressof(args))
     _check(st, "adamw_step")
+    # a graph that saved the old values must not use the new ones unnoticed
+    # (inference tensors count no versions)
+    torch.autograd.graph.increment_version([p for p in lists[0] if not p.is_inference()])

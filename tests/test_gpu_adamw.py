@@ -218,6 +218,23 @@ def test_second_moment_follows_the_gradients():
     assert abs(b - a) <= 0.1 * a
 
 
+def test_a_graph_of_the_old_parameters_is_refused():
+    """Values that autograd saved before a step must not be replaced unnoticed."""
+    import torch
+    p = torch.ones(300, device="cuda", requires_grad=True)
+    y = (p * p).sum()
+    with torch.inference_mode():
+        q = torch.ones(40, device="cuda")
+    params = [p, q]
+    say("adamw under a live graph")
+    m, v, _, _ = bs.adamw_states(params)
+    bs.adamw_step(params, [torch.ones_like(p.detach()), torch.ones(40, device="cuda")], m, v, lr=0.5, weight_decay=0.0)
+    # 1 - 0.5 m' / sqrt(v') at step 1, eight roundings of at most 2^-24 each
+    assert abs(float(p.detach()[0]) - 0.5) < 2.0 ** -21 and abs(float(q[0]) - 0.5) < 2.0 ** -21
+    with pytest.raises(RuntimeError):
+        y.backward()
+
+
 def test_train_step_end_to_end():
     """An FP8 linear layer's step as it is used: quantise, three products, AdamW with FP8 states,
     and the new weight's codes; every stage against its reference on the stage's own inputs."""
