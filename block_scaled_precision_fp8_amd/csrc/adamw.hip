@@ -78,6 +78,9 @@ __device__ __forceinline__ uint32_t xorshift(uint32_t s) {
 
 __host__ __device__ inline void set_rates(Constants& c, double lr, double beta1, double beta2, double wd, int64_t step,
                                           uint32_t seed) {
+    // 1 - lr wd with the product rounded by itself, as the host does: contracted to an
+    // FMA on the device, a rate there and the same rate as an argument could differ
+#pragma clang fp contract(off)
     const double t = static_cast<double>(step);
     c.decay = static_cast<float>(1.0 - lr * wd);
     c.size = static_cast<float>(lr / (1.0 - pow(beta1, t)));

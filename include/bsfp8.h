@@ -454,7 +454,9 @@ typedef struct {
  * read during the call.
  *
  * Per element, in FP32 with each operation rounded once (the constants in
- * parentheses are formed in 64 bits and rounded to FP32):
+ * parentheses are formed in 64 bits, each operation rounded once, and rounded to
+ * FP32; with lr_dev or step_dev on the device, whose pow may differ from the
+ * host's in the last of the 64 bits):
  *   g  = gradient * grad_scale
  *   m' = (beta1) m + (1 - beta1) g          v' = (beta2) v + ((1 - beta2) g) g
  *   p' = (1 - lr weight_decay) p - ((lr / (1 - beta1^t)) m') / ((1 / sqrt(1 - beta2^t)) sqrt(v') + (eps))

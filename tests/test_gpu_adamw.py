@@ -261,3 +261,45 @@ def test_train_step_end_to_end():
         wq, ws = bs.fp8_quantize_block128(w, "e4m3", 128)
         for a, b in zip((wq, ws), ref.quantize(from_dev(w), "e4m3", 128)):
             assert np.array_equal(from_dev(a), b)
+
+
+def decay_cases():
+    """(lr, wd) whose 64-bit product is inexact and lands on the value that makes 1 - lr wd a tie
+    between two FP32 values: rounded by itself it rounds to even, contracted to an FMA it can go
+    the other way.  Found by construction; lr is an FP32 value."""
+    from fractions import Fraction
+    g, out = np.random.default_rng(0), []
+    while len(out) < 4:
+        tie = (2 * int(g.integers(1 << 23, 1 << 24)) + 1) * 2.0 ** -26      # in [0.25, 0.5), between two FP32 values
+        lr = float(np.float32(g.uniform(0.5, 1.0)))
+        wd = (1.0 - tie) / lr
+        left = 1 - Fraction(lr) * Fraction(wd) - Fraction(tie)
+        if lr * wd == 1.0 - tie and left and np.float32(float(Fraction(tie) + left)) != np.float32(tie):
+            out.append((lr, wd))
+    return out
+
+
+def test_rates_on_the_device_are_the_arguments_rates():
+    """The same lr and step as device scalars and as arguments: the same bits."""
+    import torch
+
+    def pair(lr, wd, step, m0):
+        got = []
+        for on_device in (False, True):
+            p, g = [torch.ones(300, device="cuda")], [torch.zeros(300, device="cuda")]
+            m, v = [torch.full((300,), m0, device="cuda")], [torch.full((300,), 1e-6, device="cuda")]
+            bs.adamw_step(p, g, m, v, lr=torch.tensor([lr], device="cuda") if on_device else lr,
+                          step=torch.tensor([step], device="cuda") if on_device else step, weight_decay=wd)
+            got.append(from_dev(p[0]))
+        return got
+
+    say("adamw_step decay rates at a tie")
+    for lr, wd in decay_cases():
+        host, dev = pair(lr, wd, 5, 0.0)
+        assert np.all(host == np.float32(1.0 - lr * wd))
+        assert np.array_equal(host, dev)
+    for step in (1, 2, 7, 50, 999, 20011, 1 << 20):
+        say(f"adamw_step rates at step {step}")
+        for lr in (1e-5, 3e-4, 0.1):
+            host, dev = pair(float(np.float32(lr)), 0.1, step, 1e-3)
+            assert np.array_equal(host, dev)
