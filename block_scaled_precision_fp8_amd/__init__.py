@@ -665,6 +665,7 @@ def adamw_states(params, state: str = "f32"):
     if state not in ("f32", "fp8"):
         raise ValueError(f"unknown state {state!r}; expected 'f32' or 'fp8'")
     dt = torch.float32 if state == "f32" else torch.uint8
+    params = list(params)               # read four times: it may be a generator
 
     def zeros():
         return [torch.zeros(p.shape, dtype=dt, device=p.device) for p in params]

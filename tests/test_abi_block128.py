@@ -130,3 +130,13 @@ def test_binding_refusals():
         with pytest.raises(ValueError):
             call()
     bs.adamw_step([], [], [], [])
+
+
+@pytest.mark.parametrize("state", ["f32", "fp8"])
+def test_states_of_a_generator(state):
+    """Parameters come as model.parameters() does: a generator, read once."""
+    import torch
+    params = [torch.zeros(3, 5), torch.zeros(300)]
+    m, v, ms, vs = bs.adamw_states((p for p in params), state)
+    assert [t.shape for t in m] == [t.shape for t in v] == [p.shape for p in params]
+    assert (ms is None and vs is None) if state == "f32" else [t.numel() for t in ms] == [t.numel() for t in vs] == [1, 3]
