@@ -303,3 +303,34 @@ def test_rates_on_the_device_are_the_arguments_rates():
         for lr in (1e-5, 3e-4, 0.1):
             host, dev = pair(float(np.float32(lr)), 0.1, step, 1e-3)
             assert np.array_equal(host, dev)
+
+
+@pytest.mark.parametrize("state", ["f32", "fp8"])
+def test_shapes_that_do_not_agree_are_refused(state):
+    """A gradient or state of another shape with as many elements: refused, nothing written.  Flat ones
+    are taken: the same result."""
+    import torch
+    def fresh():
+        t = make([600], state, torch.float32, torch.float32, 8)
+        for k in "pgmv":
+            t[k] = [t[k][0].view(20, 30)]
+        return t
+
+    def go(t):
+        fp8 = state == "fp8"
+        bs.adamw_step(t["p"], t["g"], t["m"], t["v"], t["ms"] if fp8 else None, t["vs"] if fp8 else None, step=2,
+                      seed=4, **HP)
+
+    t = fresh()
+    say(f"adamw_step shapes {state}")
+    for k, name in (("g", "grads"), ("m", "m"), ("v", "v")):
+        for shape in ((30, 20), (1, 600), (20, 30, 1)):
+            with pytest.raises(ValueError, match=rf"{name}\[0\] has shape"):
+                go({**t, k: [t[k][0].view(shape)]})
+    want = fresh()
+    assert all(torch.equal(a, b) for k in t for a, b in zip(t[k], want[k]))
+    go(want)
+    for flat in ("g", "p", "gmv"):
+        t = fresh()
+        go({**t, **{k: [t[k][0].view(-1)] for k in flat}})
+        assert all(torch.equal(a, b) for k in t for a, b in zip(t[k], want[k]))
