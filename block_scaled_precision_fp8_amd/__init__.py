@@ -543,6 +543,13 @@ def _call(device, fn, *args) -> int:
         return fn(*args, torch._C._cuda_getCurrentRawStream(index))
 
 
+def _written(*tensors) -> None:
+    """Counts a write in the tensors' autograd versions: a graph that saved the old values must
+    not use the new ones unnoticed.  (Inference tensors count no versions and are passed over.)"""
+    import torch
+    torch.autograd.graph.increment_version(tensors)
+
+
 def block128_scale_shape(rows: int, k: int, block_rows: int) -> Tuple[int, int, int]:
     """Shape of the E8M0 scale bytes of a rows x k operand: [ceil(k / 512)][scale rows][4]."""
     return (k + 511) // 512, (rows + block_rows - 1) // block_rows, 4
@@ -610,6 +617,9 @@ def fp8_quantize_block128(x, fmt: str = "e4m3", block_rows: int = 1, rows: bool 
                    block_rows, f, p[0].data_ptr() if p else 0, p[1].data_ptr() if p else 0,
                    q[0].data_ptr() if q else 0, q[1].data_ptr() if q else 0)
         _check(st, "fp8_quantize_block128")
+        given = [t for t in (codes, scales, codes_t, scales_t) if t is not None]
+        if given:
+            _written(*given)
     return p + q
 
 
@@ -637,7 +647,8 @@ def scaled_gemm_block128(a, a_scales, b, b_scales, a_fmt: str = "e4m3", b_fmt: s
     for t, name, r, br in ((a_scales, "a_scales", M, a_block_rows), (b_scales, "b_scales", N, b_block_rows)):
         if t.shape != ((K + 511) // 512, (r + br - 1) // br, 4):
             raise ValueError(f"{name} must have shape {block128_scale_shape(r, K, br)}, got {tuple(t.shape)}")
-    if d is None and c is None and beta == 0.0:
+    given = d is not None
+    if not given and c is None and beta == 0.0:
         _key(OUTS, out, "output type")
         d, cp, ldc = torch.empty((M, N), dtype=getattr(torch, _OUT_DTYPES[out]), device=dev), 0, 0
     else:
@@ -647,6 +658,8 @@ def scaled_gemm_block128(a, a_scales, b, b_scales, a_fmt: str = "e4m3", b_fmt: s
                    a_block_rows, fb, b.data_ptr(), b_scales.data_ptr(), b_block_rows, alpha, cp, ldc, beta,
                    OUTS[out], d.data_ptr(), d.stride(0) if M > 1 else N)
         _check(st, "scaled_gemm_block128")
+        if given:
+            _written(d)
     return d
 
 
@@ -776,6 +789,4 @@ def adamw_step(params, grads, m, v, m_scales=None, v_scales=None, *, lr=1e-3, be
     st = _call(dev, lib().adamw_step, flat.buffer_info()[0], count, types[p0.dtype], types[g0.dtype],
                1 if fp8 else 0, ctypes.addressof(args))
     _check(st, "adamw_step")
-    # a graph that saved the old values must not use the new ones unnoticed
-    # (inference tensors count no versions)
-    torch.autograd.graph.increment_version([p for p in lists[0] if not p.is_inference()])
+    _written(*lists[0], *lists[2], *lists[3], *(lists[4] + lists[5] if fp8 else ()))

@@ -334,3 +334,15 @@ def test_shapes_that_do_not_agree_are_refused(state):
         t = fresh()
         go({**t, **{k: [t[k][0].view(-1)] for k in flat}})
         assert all(torch.equal(a, b) for k in t for a, b in zip(t[k], want[k]))
+
+
+@pytest.mark.parametrize("state", ["f32", "fp8"])
+def test_states_count_the_step_in_their_versions(state):
+    import torch
+    p, g = [torch.ones(300, device="cuda")], [torch.ones(300, device="cuda")]
+    states = bs.adamw_states(p, state)
+    say(f"adamw_step versions {state}")
+    kept = [p[0]] + [t[0] for t in states if t is not None]
+    before, g0 = [t._version for t in kept], g[0]._version
+    bs.adamw_step(p, g, *states)
+    assert [t._version for t in kept] == [n + 1 for n in before] and g[0]._version == g0

@@ -384,3 +384,27 @@ def test_stream_and_graph():
         torch.cuda.synchronize()
         eager = bs.scaled_gemm_block128(*bs.fp8_quantize_block128(x, "e4m3", 1), wq, ws)
         assert torch.equal(out, eager)
+
+
+def test_writes_count_in_autograd_versions():
+    """A graph that saved a tensor which a call then writes refuses to use the new values."""
+    import torch
+    x = values(40, 96, torch.float32, 1).cuda()
+    q, s = bs.fp8_quantize_block128(x)
+    w = torch.ones(40, 40, device="cuda", requires_grad=True)
+    for beta in (0.0, 1.0):
+        d = torch.ones(40, 40, device="cuda")
+        y = (w * d).sum()
+        say(f"gemm_block128 into a saved tensor, beta {beta}")
+        bs.scaled_gemm_block128(q, s, q, s, b_block_rows=1, out="f32", c=d, beta=beta, d=d)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    say("quantize_block128 into given outputs")
+    outs = bs.fp8_quantize_block128(x, "e4m3", 1, True, True)
+    before = [t._version for t in outs]
+    bs.fp8_quantize_block128(x, "e4m3", 1, True, True, *outs)
+    assert [t._version for t in outs] == [n + 1 for n in before]
+    with torch.inference_mode():
+        d = torch.zeros(40, 40, device="cuda")      # counts no versions
+    bs.scaled_gemm_block128(q, s, q, s, b_block_rows=1, out="f32", d=d)
+    assert from_dev(d).any()
