@@ -1,13 +1,14 @@
 // api.hip -- the C ABI of libbsfp8 (declared in include/bsfp8.h).
 // Validates every argument on the host, then launches; a non-OK status means
-// nothing was launched.  No allocation, no synchronisation, no global state.
+// nothing was launched.  No device memory is allocated, nothing is synchronised, there
+// is no global state.  (adamw_step takes host memory for its check of many tensors.)
 #include "internal.h"
 
 #include <algorithm>
 #include <cmath>
 #include <limits>
+#include <memory>
 #include <new>
-#include <vector>
 
 namespace {
 
@@ -350,51 +351,51 @@ bsfp8_status adamw_step(const bsfp8_adamw_tensor* tensors, int64_t count, bsfp8_
     const int64_t ps = p_type == BSFP8_OUT_F32 ? 4 : 2, gs = g_type == BSFP8_OUT_F32 ? 4 : 2, ss = fp8 ? 1 : 4;
     // byte ranges that are written, and those that are only read (gradients, device scalars)
     struct Range { uintptr_t at, end; bool written; };
-    std::vector<Range> ranges;
-    try {
-        ranges.reserve(static_cast<size_t>(count) * 6 + 4);
-        for (int64_t i = 0; i < count; ++i) {
-            const bsfp8_adamw_tensor& t = tensors[i];
-            if (t.n < 0 || t.n > (int64_t(1) << 40)) return BSFP8_ERR_INVALID_ARG;
-            if (t.n == 0) continue;
-            if (!t.p || !t.g || !t.m || !t.v || (fp8 && (!t.m_scales || !t.v_scales))) return BSFP8_ERR_INVALID_ARG;
-            if (!aligned(t.p, ps) || !aligned(t.g, gs) || !aligned(t.m, ss) || !aligned(t.v, ss))
-                return BSFP8_ERR_INVALID_ARG;
-            auto add = [&](const void* p, int64_t bytes, bool w) {
-                const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-                ranges.push_back({a, a + static_cast<uintptr_t>(bytes), w});
-            };
-            add(t.p, t.n * ps, true);
-            add(t.g, t.n * gs, false);
-            add(t.m, t.n * ss, true);
-            add(t.v, t.n * ss, true);
-            if (fp8) {
-                add(t.m_scales, (t.n + 127) / 128, true);
-                add(t.v_scales, (t.n + 127) / 128, true);
-            }
-        }
-        if (!ranges.empty()) {
-            // read by every workgroup, while others already write
-            auto scalar = [&](const void* p, uintptr_t bytes) {
-                const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-                if (p) ranges.push_back({a, a + bytes, false});
-            };
-            scalar(args->lr_dev, 4);
-            scalar(args->step_dev, 8);
-            scalar(args->grad_scale, 4);
-            scalar(args->found_inf, 4);
-        }
-        std::sort(ranges.begin(), ranges.end(), [](const Range& x, const Range& y) { return x.at < y.at; });
-    } catch (const std::bad_alloc&) {
-        return BSFP8_ERR_INVALID_ARG;
+    // on the stack for up to kLocalRanges (64 tensors with FP8 states), else on the heap
+    constexpr size_t kLocalRanges = 6 * 64 + 4;
+    Range local[kLocalRanges];
+    std::unique_ptr<Range[]> heap;
+    const size_t room = static_cast<size_t>(count) * (fp8 ? 6 : 4) + 4;
+    if (room > kLocalRanges) {
+        heap.reset(new (std::nothrow) Range[room]);
+        if (!heap) return BSFP8_ERR_NO_MEMORY;
     }
+    Range* const ranges = heap ? heap.get() : local;
+    size_t used = 0;
+    auto add = [&](const void* p, int64_t bytes, bool w) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        ranges[used++] = {at, at + static_cast<uintptr_t>(bytes), w};
+    };
+    for (int64_t i = 0; i < count; ++i) {
+        const bsfp8_adamw_tensor& t = tensors[i];
+        if (t.n < 0 || t.n > (int64_t(1) << 40)) return BSFP8_ERR_INVALID_ARG;
+        if (t.n == 0) continue;
+        if (!t.p || !t.g || !t.m || !t.v || (fp8 && (!t.m_scales || !t.v_scales))) return BSFP8_ERR_INVALID_ARG;
+        if (!aligned(t.p, ps) || !aligned(t.g, gs) || !aligned(t.m, ss) || !aligned(t.v, ss))
+            return BSFP8_ERR_INVALID_ARG;
+        add(t.p, t.n * ps, true);
+        add(t.g, t.n * gs, false);
+        add(t.m, t.n * ss, true);
+        add(t.v, t.n * ss, true);
+        if (fp8) {
+            add(t.m_scales, (t.n + 127) / 128, true);
+            add(t.v_scales, (t.n + 127) / 128, true);
+        }
+    }
+    if (used == 0) return BSFP8_OK;
+    // read by every workgroup, while others already write
+    if (args->lr_dev) add(args->lr_dev, 4, false);
+    if (args->step_dev) add(args->step_dev, 8, false);
+    if (args->grad_scale) add(args->grad_scale, 4, false);
+    if (args->found_inf) add(args->found_inf, 4, false);
+    std::sort(ranges, ranges + used, [](const Range& x, const Range& y) { return x.at < y.at; });
     // the furthest ends so far of written and of read ranges
     uintptr_t wend = 0, rend = 0;
-    for (const Range& r : ranges) {
+    for (size_t i = 0; i < used; ++i) {
+        const Range& r = ranges[i];
         if (r.at < wend || (r.written && r.at < rend)) return BSFP8_ERR_INVALID_ARG;
         (r.written ? wend : rend) = std::max(r.written ? wend : rend, r.end);
     }
-    if (ranges.empty()) return BSFP8_OK;
     return from_hip(bsfp8::launch_adamw(tensors, count, p_type, g_type, state, *args, stream));
 }
 
@@ -423,6 +424,7 @@ const char* bsfp8_status_string(bsfp8_status s) {
     case BSFP8_ERR_INVALID_ARG: return "BSFP8_ERR_INVALID_ARG";
     case BSFP8_ERR_UNSUPPORTED: return "BSFP8_ERR_UNSUPPORTED";
     case BSFP8_ERR_HIP: return "BSFP8_ERR_HIP";
+    case BSFP8_ERR_NO_MEMORY: return "BSFP8_ERR_NO_MEMORY";
     default: return "BSFP8_ERR_UNKNOWN";
     }
 }

@@ -2,8 +2,9 @@
  * bsfp8.h -- block-scaled FP8 / MXFP4 quantisation and GEMM on AMD MI355X (gfx950).
  *
  * A small C ABI over hand-written HIP kernels.  Every pointer argument is a
- * DEVICE pointer owned by the caller; the library never allocates, frees or
- * synchronises.  Every call is asynchronous on `stream` (0 = the null stream).
+ * DEVICE pointer owned by the caller; the library never allocates or frees
+ * device memory and never synchronises (adamw_step takes host memory during the
+ * call to check more than about 64 tensors).  Every call is asynchronous on `stream` (0 = the null stream).
  * All argument checks run on the host before anything is launched: a call
  * that returns a status other than BSFP8_OK has launched nothing.  After a
  * launch the HIP launch error, if any, is returned as BSFP8_ERR_HIP.  No
@@ -36,7 +37,8 @@ typedef enum {
     BSFP8_OK = 0,
     BSFP8_ERR_INVALID_ARG = 1,  /* null pointer, negative size, K not a multiple of 32, ld < k, ... */
     BSFP8_ERR_UNSUPPORTED = 2,  /* undefined enum value or format mix, tile_rows != 128 */
-    BSFP8_ERR_HIP = 3           /* the HIP runtime reported a launch error */
+    BSFP8_ERR_HIP = 3,          /* the HIP runtime reported a launch error */
+    BSFP8_ERR_NO_MEMORY = 4     /* no host memory for a call's check (adamw_step) */
 } bsfp8_status;
 
 typedef enum {
@@ -475,7 +477,8 @@ typedef struct {
  *
  * beta1, beta2 in [0, 1); eps >= 0; all finite.  The p, m, v and scale arrays
  * of a call must not overlap each other, the gradients or the scalars that args
- * points to (BSFP8_ERR_INVALID_ARG).  Infinities and NaN in gradients spread to p, m and
+ * points to (BSFP8_ERR_INVALID_ARG; BSFP8_ERR_NO_MEMORY where the check of many
+ * tensors finds no host memory).  Infinities and NaN in gradients spread to p, m and
  * v; with FP8 states to the whole block of 128 (scale byte 255): use found_inf.
  */
 bsfp8_status adamw_step(const bsfp8_adamw_tensor* tensors, int64_t count, bsfp8_out p_type, bsfp8_out g_type,

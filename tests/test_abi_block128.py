@@ -140,3 +140,36 @@ def test_states_of_a_generator(state):
     m, v, ms, vs = bs.adamw_states((p for p in params), state)
     assert [t.shape for t in m] == [t.shape for t in v] == [p.shape for p in params]
     assert (ms is None and vs is None) if state == "f32" else [t.numel() for t in ms] == [t.numel() for t in vs] == [1, 3]
+
+
+def test_adamw_without_host_memory():
+    """The overlap check of many tensors sorts their ranges in host memory; without it the call says
+    so instead of blaming its arguments.  (The last two tensors share their parameters, so that the
+    call is refused either way; in a process of its own, whose address space is limited for the call.)"""
+    import subprocess
+    import sys
+    code = """
+import ctypes, resource, struct, sys
+import block_scaled_precision_fp8_amd as bs
+L = bs.lib()
+def status(count, leave):
+    at = 1 << 40
+    rows = [struct.pack("<7q", at + 64 * i, at + 64 * i + 16, at + 64 * i + 32, at + 64 * i + 48, 0, 0, 1) for i in range(count)]
+    rows[-1] = rows[-2]
+    t = ctypes.create_string_buffer(b"".join(rows))
+    del rows
+    a = bs._AdamWArgs(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, step=1)
+    old = resource.getrlimit(resource.RLIMIT_AS)
+    if leave:
+        pages = int(open("/proc/self/statm").read().split()[0])
+        resource.setrlimit(resource.RLIMIT_AS, (pages * 4096 + leave, old[1]))
+    got = L.adamw_step(ctypes.addressof(t), count, 0, 0, 0, ctypes.addressof(a), None)
+    resource.setrlimit(resource.RLIMIT_AS, old)
+    return got
+for case in ((20, 0), (90, 0), (97, 0), (98, 0), (2000, 0), (1 << 20, 0), (1 << 20, 1 << 20)):
+    print(status(*case), end=" ")
+"""
+    root = bs.__file__.rsplit("/", 2)[0]
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=100)
+    assert out.stdout.split() == ["1"] * 6 + ["4"], out.stdout + out.stderr
+    assert bs.lib().bsfp8_status_string(4) == b"BSFP8_ERR_NO_MEMORY"
