@@ -405,10 +405,18 @@ bsfp8_status fp8_quantize_block128(const void* x, bsfp8_out x_type, int64_t rows
  *
  * 16-bit outputs run on the block-scaled FP8 matrix instruction, which takes
  * the E8M0 bytes itself; FP32 output widens the codes, times their scale, to
- * bf16 and uses the bf16 instruction (exact for dequantised magnitudes of
- * 2^-126 and more; smaller ones lose bits, those below 2^-133 count as zero).
- * Accuracy as for scaled_gemm_ex.  The kernel form is chosen by the sizes and
- * the output type alone, and no sum depends on timing: equal calls give equal
+ * bf16 and uses the bf16 instruction (exact for dequantised magnitudes from
+ * 2^-126 to below 2^128; smaller ones lose bits, those below 2^-133 count as
+ * zero; 2^128 and more, beyond FP32 too, count as infinite where 16-bit outputs
+ * multiply them out: fp8_quantize_block128 writes such codes for |x| above
+ * 0.93 2^128).
+ * Accuracy as for scaled_gemm_ex.  For 16-bit outputs the instruction keeps 13
+ * fraction bits of each group of 8 products: before it is rounded to the output
+ * type, D is within 7 2^-13 of sum |a b| besides the FP32 accumulator's
+ * roundings.  That worst case is above half a step of FP16 (2^-11): results that
+ * need FP16's last bit take FP32 output.
+ * The kernel form is chosen by the sizes and the output type alone, and no sum
+ * depends on timing: equal calls give equal
  * bits.
  */
 bsfp8_status scaled_gemm_block128(int64_t M, int64_t N, int64_t K, bsfp8_format a_fmt, const void* a,

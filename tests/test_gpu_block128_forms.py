@@ -157,6 +157,23 @@ def test_ends_of_the_scales(name, tiles, M, N, K, out, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("name,tiles,M,N,K", [c[:5] for c in cases(True, ("bf16",))])
+def test_magnitudes_beyond_fp32(name, tiles, M, N, K):
+    """Dequantised magnitudes of 2^128 and more, as the quantiser writes them for values next to FP32's
+    largest: 16-bit outputs multiply them out, FP32 output counts them as infinite."""
+    import torch
+    x, w = torch.ones(M, K, device="cuda"), torch.full((N, K), 2.0 ** -100, device="cuda")
+    x[M - 1] = 3.4e38
+    say(f"gemm_block128 {name} x{tiles} {M}x{N}x{K} beyond FP32")
+    t = bs.fp8_quantize_block128(x) + bs.fp8_quantize_block128(w, block_rows=128)
+    d = bs.scaled_gemm_block128(*t)
+    # 256 2^120 2^-100 K: bf16 rounds K 2^28 by at most half a step, the sum by tol
+    assert bool(((d[M - 1].double() / (K * 2.0 ** 28) - 1).abs() <= tol("bf16", K)).all())
+    d = bs.scaled_gemm_block128(*t, out="f32")
+    assert not bool(d[M - 1].isfinite().any()) and bool(d[:M - 1].isfinite().all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("name,tiles,M,N,K,out", cases(True))
 def test_odd_addresses(name, tiles, M, N, K, out):
     """D one element into a buffer, with an odd row stride: no 16-byte stores; the same bits."""
