@@ -578,7 +578,8 @@ def fp8_quantize_block128(x, fmt: str = "e4m3", block_rows: int = 1, rows: bool 
     """Quantise a rows x k CUDA tensor (float32, bfloat16 or float16, unit column stride)
     to FP8 codes with one E8M0 scale per 1 x 128 or 128 x 128 block.  Returns (codes,
     scales) of x (rows=True), of x^T (transposed=True), or all four, from one read of x.
-    Codes are rows x kp, kp = k rounded up to a multiple of 32 (zeros past k); scales as
+    Codes are rows x kp, kp = k rounded up to a multiple of 32 (zeros past k, but
+    NaN codes in a block with an infinity or a NaN); scales as
     block128_scale_shape says, bytes e + 127."""
     import torch
     types = _element_types()

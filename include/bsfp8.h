@@ -358,8 +358,9 @@ bsfp8_status scaled_gemm_quantize_a(int64_t M, int64_t N, int64_t K, const float
  * transpose has the same scales.
  *
  * Code matrices are rows x kp bytes with row stride kp = k rounded up to a
- * multiple of 32; columns k .. kp-1 hold zero codes, so any k is accepted and
- * kp is the K of the GEMM.  Scale bytes lie in words of four K blocks,
+ * multiple of 32; columns k .. kp-1 hold zero codes (NaN codes where their block
+ * holds an infinity or a NaN), so any k is accepted and kp is the K of the GEMM.
+ * Scale bytes lie in words of four K blocks,
  * [ceil(k / 512)][R][4] with R = rows (1 x 128) or ceil(rows / 128)
  * (128 x 128): byte (g, r, j) is the scale of K block 4 g + j of scale row r.
  * The words are 4-byte aligned.

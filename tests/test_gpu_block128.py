@@ -408,3 +408,18 @@ def test_writes_count_in_autograd_versions():
         d = torch.zeros(40, 40, device="cuda")      # counts no versions
     bs.scaled_gemm_block128(q, s, q, s, b_block_rows=1, out="f32", d=d)
     assert from_dev(d).any()
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_quantize_padding_codes(fmt, block_rows):
+    """Columns k .. kp - 1: zeros, but NaN codes in a block with a non-finite value."""
+    import torch
+    x = torch.ones(130, 140)
+    x[1, 139] = float("inf")
+    say(f"quantize_block128 padding block_rows={block_rows} {fmt}")
+    for transposed in (False, True):
+        y = x.t().contiguous() if transposed else x
+        codes = from_dev(bs.fp8_quantize_block128(y.cuda(), fmt, block_rows, not transposed, transposed)[0])
+        bad = np.arange(130) // block_rows == 1 // block_rows
+        assert codes.shape == (130, 160) and np.all(codes[bad, 128:] == 0x7F) and not codes[~bad, 140:].any()

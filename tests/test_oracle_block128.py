@@ -115,3 +115,13 @@ def test_round_bf16():
     x = np.array([1.0, 1.0 + 2.0 ** -8, -1.0 - 2.0 ** -8], dtype=np.float32)
     assert ref.round_bf16(x, np.zeros(3, np.uint64)).tolist() == [1.0, 1.0, -1.0]
     assert ref.round_bf16(x, np.full(3, 0x8000, np.uint64)).tolist() == [1.0, 1.0 + 2.0 ** -7, -1.0 - 2.0 ** -7]
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_padding_codes(block_rows):
+    """Columns k .. kp - 1: zeros, but NaN codes in a block with a non-finite value."""
+    x = np.ones((130, 140), dtype=np.float32)
+    x[1, 139] = np.inf
+    codes, scales = ref.quantize(x, "e4m3", block_rows)
+    bad = np.arange(130) // block_rows == 1 // block_rows
+    assert codes.shape == (130, 160) and np.all(codes[bad, 128:] == 0x7F) and not codes[~bad, 140:].any()
