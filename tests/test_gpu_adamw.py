@@ -346,3 +346,41 @@ def test_states_count_the_step_in_their_versions(state):
     before, g0 = [t._version for t in kept], g[0]._version
     bs.adamw_step(p, g, *states)
     assert [t._version for t in kept] == [n + 1 for n in before] and g[0]._version == g0
+
+
+@pytest.mark.parametrize("state", ["f32", "fp8"])
+@pytest.mark.parametrize("p_type", ["float32", "bfloat16"])
+def test_non_finite_values_stay_in_their_places(state, p_type):
+    """NaN and infinities in gradients and parameters: NaN or infinite in the same elements of p, m and
+    v (FP8 states: in the whole block of 128 of m and v), every other element as without them."""
+    import torch
+    fp8, dt, n = state == "fp8", getattr(torch, p_type), 700
+    t, u = (make([n], state, dt, torch.float32, 4) for _ in range(2))
+    inf, nan = float("inf"), float("nan")
+    for i, x in ((130, nan), (300, inf), (301, -inf)):
+        t["g"][0][i] = x
+    for i, x in ((3, nan), (400, inf), (401, -inf)):
+        t["p"][0][i] = x
+    if p_type == "bfloat16":
+        t["p"][0].view(torch.int16)[4] = 0x7F81         # a NaN whose set bit is the lowest
+    say(f"adamw_step non-finite {state} {p_type}")
+    for x in (t, u):
+        bs.adamw_step(x["p"], x["g"], x["m"], x["v"], x["ms"] if fp8 else None, x["vs"] if fp8 else None, step=2,
+                      seed=5, **HP)
+    p, q = from_dev(t["p"][0]), from_dev(u["p"][0])
+    nans = [3, 130, 300, 301] + ([4] if p_type == "bfloat16" else [])
+    assert np.isnan(p[nans]).all() and p[400] == inf and p[401] == -inf
+    keep = np.setdiff1d(np.arange(n), nans + [400, 401])
+    assert np.array_equal(p[keep], q[keep])
+    if fp8:
+        for k in "mv":
+            c, s = from_dev(t[k][0]), from_dev(t[k + "s"][0])
+            d, e = from_dev(u[k][0]), from_dev(u[k + "s"][0])
+            assert s.tolist() == [e[0], 255, 255, *e[3:]] and np.all(c[128:384] == 0x7F)
+            keep = np.r_[0:128, 384:n]
+            assert np.array_equal(c[keep], d[keep])
+    else:
+        m, v = from_dev(t["m"][0]), from_dev(t["v"][0])
+        assert np.isnan(m[130]) and np.isnan(v[130]) and m[300] == inf and m[301] == -inf and np.all(v[300:302] == inf)
+        keep = np.setdiff1d(np.arange(n), [130, 300, 301])
+        assert np.array_equal(m[keep], from_dev(u["m"][0])[keep]) and np.array_equal(v[keep], from_dev(u["v"][0])[keep])
