@@ -699,9 +699,9 @@ def _scalar_ptr(t, name: str, dtype, device) -> int:
     return t.data_ptr()
 
 
-def _same_elements(t, p) -> bool:
-    """t's elements are p's, one by one: the same shape, or one of the two flat."""
-    return t.shape == p.shape or (t.numel() == p.numel() and (t.dim() <= 1 or p.dim() <= 1))
+def _same_order(t, p) -> bool:
+    """t, of as many elements as p, has them in p's places: the same shape, or one of the two flat."""
+    return t.shape == p.shape or t.dim() <= 1 or p.dim() <= 1
 
 
 def _adamw_complain(lists, p_dtype, g_dtype, state_dtype, dev):
@@ -716,7 +716,7 @@ def _adamw_complain(lists, p_dtype, g_dtype, state_dtype, dev):
             if t.numel() != n or not t.is_contiguous():
                 raise ValueError(f"{names[j]}[{i}] must be contiguous with {n} elements, got {tuple(t.shape)} "
                                  f"(contiguous: {t.is_contiguous()})")
-            if j < 4 and not _same_elements(t, row[0]):
+            if j < 4 and not _same_order(t, row[0]):
                 raise ValueError(f"{names[j]}[{i}] has shape {tuple(t.shape)}, params[{i}] {tuple(row[0].shape)}: "
                                  "shapes must agree, or one of the two be flat")
     raise ValueError("tensors do not fit together")
@@ -728,8 +728,9 @@ def adamw_step(params, grads, m, v, m_scales=None, v_scales=None, *, lr=1e-3, be
     """One AdamW step over lists of tensors, in place.
 
     params: contiguous float32 or bfloat16 tensors of one dtype; grads: float32, bfloat16 or
-    float16, of the same shapes (or flat: 1-D with as many elements).  m, v, alike: float32 moments, or (with m_scales and v_scales, see
-    adamw_states) uint8 E4M3 codes of m and sqrt(v), rounded stochastically.  bfloat16
+    float16, of the same shapes (or flat: 1-D with as many elements).  m, v, alike: float32
+    moments, or (with m_scales and v_scales, see adamw_states) uint8 E4M3 codes of m and
+    sqrt(v), rounded stochastically.  bfloat16
     parameters are rounded stochastically too; the random bits depend on (seed, step,
     position in the list, element).
 
@@ -762,9 +763,9 @@ def adamw_step(params, grads, m, v, m_scales=None, v_scales=None, *, lr=1e-3, be
                 if t.dtype is not dt or t.get_device() != index or not t.is_contiguous():
                     raise ValueError
         sizes = [t.numel() for t in lists[0]]
-        shapes = [t.shape for t in lists[0]]
+        wide = [(i, t) for i, t in enumerate(lists[0]) if t.dim() > 1]
         for x in lists[1:4]:
-            if [t.shape for t in x] != shapes and not all(map(_same_elements, x, lists[0])):
+            if [t.numel() for t in x] != sizes or not all(_same_order(x[i], t) for i, t in wide):
                 raise ValueError
         for x in lists[4:]:
             if [t.numel() for t in x] != [(n + 127) // 128 for n in sizes]:
