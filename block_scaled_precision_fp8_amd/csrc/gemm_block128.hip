@@ -9,7 +9,7 @@
 // its row's E8M0 byte, so the sum over all of K stays in the accumulators and
 // no VALU work is done per block.  FP32 output needs more than that
 // instruction's 13 fraction bits per group of 8 products: there the codes are
-// widened to bf16 with their scale (exact) and multiplied by
+// widened to bf16 with their scale (exact in bf16's normal range) and multiplied by
 // v_mfma_f32_32x32x16_bf16, which keeps 24.
 //
 // Scale bytes lie in words of four K blocks, [ceil(K / 512)][scale rows][4]: a
@@ -181,7 +181,9 @@ hipError_t launch_typed(int64_t M, int64_t N, int64_t K, const uint8_t* a, const
 // 256 x 128, 256 x 256): 256 x 4096 x 4096: 16.5, 17.3, 20.4, 23.3, 37.5;
 // 1111 x 4000 x 4064: 95, 39, 28.3, 32.4, 43.8; 2048 x 4096 x 4096: 147, 33.7,
 // 44.6, 32.9, 43.5; 1024 x 14336 x 4096: 187, 60, 65, 55.7, 48.6; FP32
-// 1024 x 1024 x 16384: 75, 101, 131, 163, 282.
+// 1024 x 1024 x 16384: 75, 101, 131, 163, 282.  `stage` and `tile` come from one
+// round; over several they are low: 1700 x 14336 x 4096 (four of 192 x 128) is put
+// at 87 and takes 109, 4608 x 12288 x 4096 (seven of 256 x 128) 186 and 205.
 int choose_form(int64_t M, int64_t N, int64_t K, int out) {
     struct Cost { int rows_a, rows_b; double stage, stage_f32, tile; };
     static constexpr Cost kCost[4] = {

@@ -19,8 +19,15 @@
 // are compile-time (the loop body is four stages): a loop of one stage with
 // addresses moved on at run time took 4% longer (FFN 696 -> 726 us), and with
 // the three buffers that it allows the 192 x 128 tile got no faster (28.3, then
-// 29.2 us for 1111 x 4000 x 4064): what holds the smaller tiles is the CU's
-// 64 bytes per cycle from L2, not latency.
+// 29.2 us for 1111 x 4000 x 4064).
+//
+// What holds the smaller tiles is their loads: 1111 x 4000 x 4096, one tile of
+// 192 x 128 on each of 192 CUs, takes 25 to 27 us, 23 with the MFMAs left out and
+// 17 to 20 with the direct loads left out.  A stage's 40 KB then take 0.57 us, 30
+// bytes per cycle and CU at 2.4 GHz, half of what a CU can take from L2.  Code rows whose
+// length is no multiple of 128 start within a line, so that a load of 128 bytes
+// touches two: K = 4064 takes 31 us, 29 of them without MFMAs (36 and 36, against
+// 28 and 27 for K = 4096, with operands from HBM).
 //
 // With more tiles than workgroups the grid is persistent: the loads run on into
 // the next tile's first stages while the last ones of this tile are computed
