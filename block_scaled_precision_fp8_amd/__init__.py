@@ -24,6 +24,13 @@ Functions (same names as the C ABI):
                  -> (codes, scales), those of x^T, or both
   scaled_gemm_block128(a, a_scales, b, b_scales, a_fmt, b_fmt, a_block_rows=1,
                  b_block_rows=128, out="bf16", ...) -> d
+  rmsnorm_quantize_block128(x, weight=None, residual=None, eps=..., fmt="e4m3", y=None, rstd=False)
+                 -> RMSNorm(codes, scales, y, h, rstd)
+  rmsnorm_backward(dy, h, rstd, weight=None, dh=None) -> (dx, dweight)
+  fp8_quantize_grouped_block128(x, offsets, fmt="e4m3", index=None, rows=True, transposed=False)
+                 -> (codes, scales), those of x^T group by group, or both
+  scaled_gemm_grouped_block128(a, a_scales, b, b_scales, offsets, ...) -> d (rows by expert)
+  scaled_gemm_grouped_wgrad_block128(a, a_scales, b, b_scales, offsets, ...) -> d (one matrix per expert)
   adamw_step(params, grads, m, v, m_scales=None, v_scales=None, lr=..., ...) (in place)
   adamw_states(params, state="f32"|"fp8") -> zeroed (m, v, m_scales, v_scales)
 """
@@ -32,7 +39,7 @@ from __future__ import annotations
 import array
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("BSFP8_LIB", os.path.join(_HERE, "libbsfp8.so"))
@@ -92,6 +99,26 @@ def lib() -> ctypes.CDLL:
     L.scaled_gemm_block128.argtypes = [i64, i64, i64, c_int, vp, vp, c_int, c_int, vp, vp, c_int,
                                        ctypes.c_float, vp, i64, ctypes.c_float, c_int, vp, i64, vp]
     L.scaled_gemm_block128.restype = c_int
+    L.rmsnorm_quantize_block128.argtypes = [vp, c_int, i64, i64, i64, vp, c_int, i64, vp, c_int, ctypes.c_float,
+                                            c_int, vp, vp, vp, c_int, i64, vp, i64, vp, vp]
+    L.rmsnorm_quantize_block128.restype = c_int
+    L.rmsnorm_backward_workspace.argtypes = [i64, i64]
+    L.rmsnorm_backward_workspace.restype = i64
+    L.rmsnorm_backward.argtypes = [vp, c_int, i64, vp, c_int, i64, vp, vp, c_int, vp, c_int, i64, i64, i64, vp, i64,
+                                   vp, c_int, vp, i64, vp]
+    L.rmsnorm_backward.restype = c_int
+    L.block128_grouped_columns.argtypes = L.block128_grouped_words.argtypes = [i64, i64]
+    L.block128_grouped_columns.restype = L.block128_grouped_words.restype = i64
+    L.fp8_quantize_grouped_block128.argtypes = [vp, c_int, i64, i64, i64, vp, i64, vp, i64, c_int, vp, vp, vp, i64,
+                                                vp, i64, vp]
+    L.fp8_quantize_grouped_block128.restype = c_int
+    L.scaled_gemm_grouped_block128.argtypes = [i64, i64, i64, i64, vp, c_int, vp, vp, c_int, vp, vp, c_int,
+                                               ctypes.c_float, vp, i64, ctypes.c_float, c_int, vp, i64, vp]
+    L.scaled_gemm_grouped_block128.restype = c_int
+    L.scaled_gemm_grouped_wgrad_block128.argtypes = [i64, i64, i64, i64, i64, vp, c_int, vp, vp, c_int, vp, vp,
+                                                     ctypes.c_float, vp, i64, i64, ctypes.c_float, c_int, vp, i64,
+                                                     i64, vp]
+    L.scaled_gemm_grouped_wgrad_block128.restype = c_int
     L.adamw_step.argtypes = [vp, i64, c_int, c_int, c_int, vp, vp]
     L.adamw_step.restype = c_int
     L.bsfp8_status_string.argtypes = [c_int]
@@ -659,6 +686,326 @@ def scaled_gemm_block128(a, a_scales, b, b_scales, a_fmt: str = "e4m3", b_fmt: s
                    a_block_rows, fb, b.data_ptr(), b_scales.data_ptr(), b_block_rows, alpha, cp, ldc, beta,
                    OUTS[out], d.data_ptr(), d.stride(0) if M > 1 else N)
         _check(st, "scaled_gemm_block128")
+        if given:
+            _written(d)
+    return d
+
+
+# ---------------------------------------------------------------------------
+# The norm, and products grouped by expert
+# ---------------------------------------------------------------------------
+def _matrix(t, name: str, dtypes, device, shape=None):
+    """A 2-D tensor (of `shape`) with unit column stride and rows that do not overlap; its row stride."""
+    _tensor(t, name, dtypes, device)
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be 2-D{'' if shape is None else f' of shape {tuple(shape)}'}, got {tuple(t.shape)}")
+    n, k = t.shape
+    ld, unit = t.stride()
+    if n and k and ((k > 1 and unit != 1) or (n > 1 and ld < k)):
+        raise ValueError(f"{name} must have unit column stride and rows that do not overlap, got strides {(ld, unit)}")
+    return ld if n > 1 else k
+
+
+def _vector(t, name: str, n: int, dtypes, device):
+    _tensor(t, name, dtypes, device)
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape ({n},), got {tuple(t.shape)}")
+    return t
+
+
+class RMSNorm(NamedTuple):
+    """What rmsnorm_quantize_block128 returns; None where it was not asked for."""
+    codes: object
+    scales: object
+    y: object
+    h: object
+    rstd: object
+
+
+def rmsnorm_quantize_block128(x, weight=None, residual=None, *, eps: float = 1e-6, fmt: Optional[str] = "e4m3",
+                              y=None, rstd=False, codes=None, scales=None, h=None) -> RMSNorm:
+    """h = x + residual (rounded to the residual's dtype), y = h / sqrt(mean(h^2) + eps) * weight, and y's
+    FP8 codes and E8M0 scales per 1 x 128 block, as fp8_quantize_block128 writes them, from one read.
+
+    x (and residual): rows x k float32, bfloat16 or float16, unit column stride; weight: [k] of any
+    of these, or None for ones.  fmt None: no codes.  y: None, an output type ("f32", "bf16", "f16")
+    or the tensor to write; rstd: True, or the float32 tensor [rows] to write, for
+    rmsnorm_backward.  h: where the sum goes (it may be residual itself); a new tensor if not
+    given, None without a residual."""
+    import torch
+    types = _element_types()
+    dtypes = tuple(types)
+    _tensor(x, "x", dtypes)
+    dev = x.device
+    ldx = _matrix(x, "x", dtypes, dev)
+    n, k = x.shape
+    if fmt is None:
+        if codes is not None or scales is not None:
+            raise ValueError("codes and scales need a format")
+        if y is None:
+            raise ValueError("fmt or y must be given")
+    f = _fp8_fmt("e4m3" if fmt is None else fmt)
+    given = [t for t in (codes, scales, h) if t is not None]
+    hp = rp = wp = yp = 0
+    ht = wt = yt = 0
+    ldr = ldh = ldy = 0
+    if residual is not None:
+        ldr = _matrix(residual, "residual", dtypes, dev, (n, k))
+        if h is None:
+            h = torch.empty((n, k), dtype=residual.dtype, device=dev)
+        ldh = _matrix(h, "h", (residual.dtype,), dev, (n, k))
+        rp, hp, ht = residual.data_ptr(), h.data_ptr(), types[residual.dtype]
+    elif h is not None:
+        raise ValueError("h is for a residual")
+    if weight is not None:
+        _vector(weight, "weight", k, dtypes, dev)
+        wp, wt = weight.data_ptr(), types[weight.dtype]
+    if y is not None:
+        if isinstance(y, str):
+            _key(OUTS, y, "output type")
+            y = torch.empty((n, k), dtype=getattr(torch, _OUT_DTYPES[y]), device=dev)
+        else:
+            given.append(y)
+        ldy = _matrix(y, "y", dtypes, dev, (n, k))
+        yp, yt = y.data_ptr(), types[y.dtype]
+    if rstd is True:
+        rstd = torch.empty((n,), dtype=torch.float32, device=dev)
+    elif rstd is False or rstd is None:
+        rstd = None
+    else:
+        given.append(_vector(rstd, "rstd", n, (torch.float32,), dev))
+    if fmt is not None:
+        shape, sshape = (n, (k + 31) // 32 * 32), block128_scale_shape(n, k, 1)
+        codes = torch.empty(shape, dtype=torch.uint8, device=dev) if codes is None else _packed(
+            codes, "codes", shape, (torch.uint8,), dev)
+        scales = torch.empty(sshape, dtype=torch.uint8, device=dev) if scales is None else _packed(
+            scales, "scales", sshape, (torch.uint8,), dev)
+    if n and k:
+        st = _call(dev, lib().rmsnorm_quantize_block128, x.data_ptr(), types[x.dtype], n, k, ldx, rp, ht, ldr, wp, wt,
+                   eps, f, 0 if codes is None else codes.data_ptr(), 0 if codes is None else scales.data_ptr(), yp, yt,
+                   ldy, hp, ldh, 0 if rstd is None else rstd.data_ptr())
+        _check(st, "rmsnorm_quantize_block128")
+        if given:
+            _written(*given)
+    return RMSNorm(codes, scales, y, h, rstd)
+
+
+def rmsnorm_backward(dy, h, rstd, weight=None, *, dh=None, dx=None, dweight=None, weight_grad: bool = True,
+                     accumulate: bool = False, workspace=None):
+    """The gradients of y = h * rstd * weight, rstd = 1 / sqrt(mean(h^2) + eps) as the forward call
+    returned it: (dx, dweight).  dx has h's dtype and is the gradient of x and of the residual;
+    dh, the gradient that reaches h along the residual, is added.  dweight is float32 [k];
+    accumulate: it is added to the one given; weight_grad False: it is not formed (None).
+    dx may be dy, h or dh itself (same dtype and row stride).  workspace: a contiguous uint8
+    tensor of rmsnorm_backward_workspace bytes for calls that should not allocate one."""
+    import torch
+    types = _element_types()
+    dtypes = tuple(types)
+    _tensor(dy, "dy", dtypes)
+    dev = dy.device
+    ldy = _matrix(dy, "dy", dtypes, dev)
+    n, k = dy.shape
+    ldh = _matrix(h, "h", dtypes, dev, (n, k))
+    _vector(rstd, "rstd", n, (torch.float32,), dev)
+    given = [t for t in (dx, dweight) if t is not None]
+    wp = wt = ap = at = lda = 0
+    if weight is not None:
+        _vector(weight, "weight", k, dtypes, dev)
+        wp, wt = weight.data_ptr(), types[weight.dtype]
+    if dh is not None:
+        lda = _matrix(dh, "dh", dtypes, dev, (n, k))
+        ap, at = dh.data_ptr(), types[dh.dtype]
+    if dx is None:
+        dx = torch.empty((n, k), dtype=h.dtype, device=dev)
+    ldx = _matrix(dx, "dx", (h.dtype,), dev, (n, k))
+    gp = sp = size = 0
+    if not weight_grad:
+        if dweight is not None or accumulate:
+            raise ValueError("dweight and accumulate need weight_grad")
+    else:
+        if dweight is None:
+            if accumulate:
+                raise ValueError("accumulate needs dweight")
+            dweight = torch.empty((k,), dtype=torch.float32, device=dev)
+        _vector(dweight, "dweight", k, (torch.float32,), dev)
+        gp, size = dweight.data_ptr(), lib().rmsnorm_backward_workspace(n, k)
+        if workspace is None:
+            workspace = torch.empty((size,), dtype=torch.uint8, device=dev)
+        _flat(workspace, "workspace", size, (torch.uint8,), dev)
+        sp = workspace.data_ptr()
+    if k and (n or weight_grad):
+        st = _call(dev, lib().rmsnorm_backward, dy.data_ptr(), types[dy.dtype], ldy, h.data_ptr(), types[h.dtype], ldh,
+                   rstd.data_ptr(), wp, wt, ap, at, lda, n, k, dx.data_ptr(), ldx, gp, 1 if accumulate else 0, sp, size)
+        _check(st, "rmsnorm_backward")
+        if given:
+            _written(*given)
+    return dx, dweight
+
+
+def rmsnorm_backward_workspace(rows: int, k: int) -> int:
+    """Bytes of workspace that rmsnorm_backward needs for the weight's gradient."""
+    return lib().rmsnorm_backward_workspace(rows, k)
+
+
+def _offsets(offsets, device) -> int:
+    """The groups of an int32 tensor of their offsets (groups + 1)."""
+    import torch
+    _tensor(offsets, "offsets", (torch.int32,), device)
+    if offsets.dim() != 1 or offsets.shape[0] < 1 or not offsets.is_contiguous():
+        raise ValueError(f"offsets must be contiguous with groups + 1 elements, got {tuple(offsets.shape)}")
+    return offsets.shape[0] - 1
+
+
+def block128_grouped_shape(rows: int, k: int, groups: int):
+    """Shapes of the codes and of the scale bytes of the transpose of `rows` rows of k columns in
+    groups of any sizes: (k, columns) and (words, k, 4)."""
+    return (k, lib().block128_grouped_columns(rows, groups)), (lib().block128_grouped_words(rows, groups), k, 4)
+
+
+def fp8_quantize_grouped_block128(x, offsets, fmt: str = "e4m3", index=None, rows: bool = True,
+                                  transposed: bool = False, codes=None, scales=None, codes_t=None, scales_t=None):
+    """fp8_quantize_block128 (1 x 128 blocks) of rows sorted into groups: group e holds sorted rows
+    offsets[e] .. offsets[e + 1] - 1 (int32, on the device).  index (int32): sorted row i is
+    row index[i] of x.  Returns (codes, scales) of the sorted rows (rows=True), of their transpose
+    (transposed=True) or all four.  In the transpose, k rows of codes, each group's columns start
+    at a multiple of 128 and its scales at a word, for scaled_gemm_grouped_wgrad_block128; the
+    shapes, enough for any group sizes, are those of block128_grouped_shape.  Rows of
+    no group, and what lies past the last group's columns, are left as they were."""
+    import torch
+    types = _element_types()
+    _tensor(x, "x", tuple(types))
+    dev = x.device
+    ld = _matrix(x, "x", tuple(types), dev)
+    source, k = x.shape
+    groups = _offsets(offsets, dev)
+    f = _fp8_fmt(fmt)
+    n = source
+    if index is not None:
+        _tensor(index, "index", (torch.int32,), dev)
+        if index.dim() != 1 or not index.is_contiguous():
+            raise ValueError("index must be 1-D and contiguous")
+        n = index.shape[0]
+    if not rows and not transposed:
+        raise ValueError("rows or transposed must be set")
+
+    def outs(want, shape, sshape, c, s, suffix):
+        if not want:
+            if c is not None or s is not None:
+                raise ValueError(f"codes{suffix} and scales{suffix} are for an orientation that is not asked for")
+            return ()
+        c = torch.empty(shape, dtype=torch.uint8, device=dev) if c is None else _packed(
+            c, "codes" + suffix, shape, (torch.uint8,), dev)
+        s = torch.empty(sshape, dtype=torch.uint8, device=dev) if s is None else _packed(
+            s, "scales" + suffix, sshape, (torch.uint8,), dev)
+        return c, s
+
+    given = [t for t in (codes, scales, codes_t, scales_t) if t is not None]
+    p = outs(rows, (n, (k + 31) // 32 * 32), block128_scale_shape(n, k, 1), codes, scales, "")
+    q = outs(transposed, *block128_grouped_shape(n, k, groups), codes_t, scales_t, "_t")
+    if n and k and groups:
+        st = _call(dev, lib().fp8_quantize_grouped_block128, x.data_ptr(), types[x.dtype], source, k, ld,
+                   0 if index is None else index.data_ptr(), n, offsets.data_ptr(), groups, f,
+                   p[0].data_ptr() if p else 0, p[1].data_ptr() if p else 0, q[0].data_ptr() if q else 0,
+                   q[0].shape[1] if q else 0, q[1].data_ptr() if q else 0, q[1].shape[0] if q else 0)
+        _check(st, "fp8_quantize_grouped_block128")
+        if given:
+            _written(*given)
+    return p + q
+
+
+def _bytes(t, name: str, dim: int, device):
+    """A contiguous uint8 tensor of `dim` dimensions."""
+    import torch
+    _tensor(t, name, (torch.uint8,), device)
+    if t.dim() != dim or not t.is_contiguous():
+        raise ValueError(f"{name} must be {dim}-D and contiguous, got shape {tuple(t.shape)}")
+    return t
+
+
+def scaled_gemm_grouped_block128(a, a_scales, b, b_scales, offsets, a_fmt: str = "e4m3", b_fmt: str = "e4m3",
+                                 b_block_rows: int = 128, out: str = "bf16", alpha: float = 1.0, c=None,
+                                 beta: float = 0.0, d=None):
+    """D[i] = alpha deq(A)[i] deq(B[e])^T + beta C[i] for the rows i of each group e, rows
+    offsets[e] .. offsets[e + 1] - 1 (int32, on the device).  a: M x K codes with scales per
+    1 x 128 block; b: [groups, N, K] codes, b_scales [groups, *block128_scale_shape(N, K, b_block_rows)].
+    Rows of no group are left as they were.  c may be d itself."""
+    fa, fb = _fp8_fmt(a_fmt), _fp8_fmt(b_fmt)
+    _block_rows(b_block_rows, "b_block_rows")
+    _bytes(a, "a", 2, None)
+    dev = a.device
+    _bytes(a_scales, "a_scales", 3, dev)
+    _bytes(b, "b", 3, dev)
+    _bytes(b_scales, "b_scales", 4, dev)
+    groups = _offsets(offsets, dev)
+    (M, K), N = a.shape, b.shape[1]
+    if b.shape[0] != groups or b.shape[2] != K:
+        raise ValueError(f"b must be {groups} x N x {K}, got {tuple(b.shape)}")
+    if a_scales.shape != block128_scale_shape(M, K, 1):
+        raise ValueError(f"a_scales must have shape {block128_scale_shape(M, K, 1)}, got {tuple(a_scales.shape)}")
+    if b_scales.shape != (groups, *block128_scale_shape(N, K, b_block_rows)):
+        raise ValueError(f"b_scales must have shape {(groups, *block128_scale_shape(N, K, b_block_rows))}, "
+                         f"got {tuple(b_scales.shape)}")
+    given = d is not None
+    d, cp, ldc = _epilogue_tensors(d, c, beta, M, N, out, dev)
+    if M and N and groups:
+        st = _call(dev, lib().scaled_gemm_grouped_block128, M, N, K, groups, offsets.data_ptr(), fa, a.data_ptr(),
+                   a_scales.data_ptr(), fb, b.data_ptr(), b_scales.data_ptr(), b_block_rows, alpha, cp, ldc, beta,
+                   OUTS[out], d.data_ptr(), d.stride(0) if M > 1 else N)
+        _check(st, "scaled_gemm_grouped_block128")
+        if given:
+            _written(d)
+    return d
+
+
+def _group_matrices(t, name: str, shape, dtype, device):
+    """A [groups, M, N] output (or C): unit column stride, rows and matrices that do not overlap; its
+    row and group strides."""
+    _tensor(t, name, (dtype,), device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    E, M, N = shape
+    group, ld, unit = t.stride()
+    ld = ld if M > 1 else N
+    if t.numel() and ((N > 1 and unit != 1) or ld < N or (E > 1 and group < (M - 1) * ld + N)):
+        raise ValueError(f"{name} must have unit column stride, and rows and matrices that do not overlap")
+    return ld, group
+
+
+def scaled_gemm_grouped_wgrad_block128(a, a_scales, b, b_scales, offsets, a_fmt: str = "e4m3", b_fmt: str = "e4m3",
+                                       out: str = "bf16", alpha: float = 1.0, c=None, beta: float = 0.0, d=None):
+    """D[e] = alpha sum over the rows i of group e of deq(A)[:, i] deq(B)[:, i]^T + beta C[e]: [groups, M, N].
+    a (M x columns) and b (N x columns) with their scales: transposes that
+    fp8_quantize_grouped_block128 wrote with the same offsets.  c may be d itself, to accumulate."""
+    import torch
+    fa, fb = _fp8_fmt(a_fmt), _fp8_fmt(b_fmt)
+    _bytes(a, "a", 2, None)
+    dev = a.device
+    _bytes(b, "b", 2, dev)
+    _bytes(a_scales, "a_scales", 3, dev)
+    _bytes(b_scales, "b_scales", 3, dev)
+    groups = _offsets(offsets, dev)
+    (M, columns), N, words = a.shape, b.shape[0], a_scales.shape[0]
+    if b.shape[1] != columns or columns % 128:
+        raise ValueError(f"a ({tuple(a.shape)}) and b ({tuple(b.shape)}) must have the same columns, a multiple of 128")
+    for t, name, rows in ((a_scales, "a_scales", M), (b_scales, "b_scales", N)):
+        if t.shape != (words, rows, 4):
+            raise ValueError(f"{name} must have shape {(words, rows, 4)}, got {tuple(t.shape)}")
+    _key(OUTS, out, "output type")
+    dt, shape, given = getattr(torch, _OUT_DTYPES[out]), (groups, M, N), d is not None
+    if not given:
+        d = torch.empty(shape, dtype=dt, device=dev)
+    ldd, d_group = _group_matrices(d, "d", shape, dt, dev)
+    cp = ldc = c_group = 0
+    if c is not None:
+        ldc, c_group = _group_matrices(c, "c", shape, dt, dev)
+        cp = c.data_ptr()
+    elif beta != 0.0:
+        raise ValueError("beta != 0 needs c")
+    if M and N and groups:
+        st = _call(dev, lib().scaled_gemm_grouped_wgrad_block128, M, N, columns, words, groups, offsets.data_ptr(), fa,
+                   a.data_ptr(), a_scales.data_ptr(), fb, b.data_ptr(), b_scales.data_ptr(), alpha, cp, ldc, c_group,
+                   beta, OUTS[out], d.data_ptr(), ldd, d_group)
+        _check(st, "scaled_gemm_grouped_wgrad_block128")
         if given:
             _written(d)
     return d

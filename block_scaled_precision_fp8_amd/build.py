@@ -15,7 +15,7 @@ SOURCES = ["api.hip", "quantize.hip", "gemm_fp8.hip", "gemm_fp8_big.hip", "gemm_
            "gemm_mxfp4.hip", "gemm_mx.hip", "quantize_block128.hip", "gemm_block128.hip", "gemm_block128_rows.hip",
            "gemm_block128_4x4.hip",
            "gemm_block128_4x2.hip", "gemm_block128_3x2.hip", "gemm_block128_2x2.hip",
-           "adamw.hip"]
+           "adamw.hip", "rmsnorm.hip", "quantize_grouped.hip", "gemm_grouped_rows.hip", "gemm_grouped_wgrad.hip"]
 
 
 def build(verbose: bool = False, jobs: int = 8) -> str:

@@ -2,6 +2,7 @@
 // Validates every argument on the host, then launches; a non-OK status means
 // nothing was launched.  No device memory is allocated, nothing is synchronised, there
 // is no global state.  (adamw_step takes host memory for its check of many tensors.)
+#include "gemm_grouped.h"
 #include "internal.h"
 
 #include <algorithm>
@@ -26,7 +27,14 @@ constexpr int64_t kOnlineMaxColumnTiles = 4;
 // fp8_quantize_block128's 128 x 128 tiles: HIP counts a launch's threads in 32
 // bits (2^24 workgroups of 256), and the grid is padded to groups of 4 x 4 tiles
 constexpr int64_t kMaxTiles = int64_t(1) << 23;
+// and 16 threads per row and 512 columns of the rows alone
+constexpr int64_t kMaxRowItems = int64_t(1) << 27;
+// the norm's kernels hold a row in the registers of at most 16 waves
+constexpr int64_t kMaxNormColumns = 32768;
+// rows, and columns padded by group, are counted in 32 bits
+constexpr int64_t kMaxGroupedRows = int64_t(1) << 30;
 
+inline uintptr_t bytes_of(int type) { return type == BSFP8_OUT_F32 ? 4 : 2; }
 inline bsfp8_status from_hip(hipError_t e) { return e == hipSuccess ? BSFP8_OK : BSFP8_ERR_HIP; }
 
 }  // namespace
@@ -334,6 +342,149 @@ bsfp8_status scaled_gemm_block128(int64_t M, int64_t N, int64_t K, bsfp8_format 
                                                 ep, stream));
 }
 
+bsfp8_status rmsnorm_quantize_block128(const void* x, bsfp8_out x_type, int64_t rows, int64_t k, int64_t ldx,
+                                       const void* residual, bsfp8_out h_type, int64_t ldr, const void* weight,
+                                       bsfp8_out w_type, float eps, bsfp8_format fmt, uint8_t* codes, uint8_t* scales,
+                                       void* y, bsfp8_out y_type, int64_t ldy, void* h, int64_t ldh, float* rstd,
+                                       hipStream_t stream) {
+    if (!is_fp8(fmt) || !is_element(x_type)) return BSFP8_ERR_UNSUPPORTED;
+    if ((residual && !is_element(h_type)) || (weight && !is_element(w_type)) || (y && !is_element(y_type)))
+        return BSFP8_ERR_UNSUPPORTED;
+    if (rows < 0 || k < 0 || rows > kI32Max || !(eps >= 0.0f) || !std::isfinite(eps)) return BSFP8_ERR_INVALID_ARG;
+    if ((codes == nullptr) != (scales == nullptr) || (residual == nullptr) != (h == nullptr)) return BSFP8_ERR_INVALID_ARG;
+    if (rows == 0 || k == 0) return BSFP8_OK;
+    if (k > kMaxNormColumns) return BSFP8_ERR_UNSUPPORTED;
+    if (!x || (!codes && !y) || ldx < k || (residual && (ldr < k || ldh < k)) || (y && ldy < k)) return BSFP8_ERR_INVALID_ARG;
+    if (!aligned(x, bytes_of(x_type)) || (residual && (!aligned(residual, bytes_of(h_type)) || !aligned(h, bytes_of(h_type)))) ||
+        (weight && !aligned(weight, bytes_of(w_type))) || (y && !aligned(y, bytes_of(y_type))) || !aligned(rstd, 4) ||
+        !aligned(codes, 16) || !aligned(scales, 4))
+        return BSFP8_ERR_INVALID_ARG;
+    return from_hip(bsfp8::launch_rmsnorm(x, x_type, rows, k, ldx, residual, h_type, ldr, weight, w_type, eps, fmt, codes,
+                                          scales, y, y_type, ldy, h, ldh, rstd, stream));
+}
+
+int64_t rmsnorm_backward_workspace(int64_t rows, int64_t k) {
+    if (rows <= 0 || k <= 0 || rows > kI32Max || k > kMaxNormColumns) return 0;
+    return bsfp8::rmsnorm_grad_workspace(rows, k);
+}
+
+bsfp8_status rmsnorm_backward(const void* dy, bsfp8_out dy_type, int64_t ldy, const void* h, bsfp8_out h_type,
+                              int64_t ldh, const float* rstd, const void* weight, bsfp8_out w_type, const void* dh,
+                              bsfp8_out dh_type, int64_t lddh, int64_t rows, int64_t k, void* dx, int64_t ldx,
+                              float* dweight, int accumulate, void* workspace, int64_t workspace_bytes,
+                              hipStream_t stream) {
+    if (!is_element(dy_type) || !is_element(h_type)) return BSFP8_ERR_UNSUPPORTED;
+    if ((weight && !is_element(w_type)) || (dh && !is_element(dh_type))) return BSFP8_ERR_UNSUPPORTED;
+    if (rows < 0 || k < 0 || rows > kI32Max || (accumulate != 0 && accumulate != 1)) return BSFP8_ERR_INVALID_ARG;
+    if (k == 0) return BSFP8_OK;
+    if (k > kMaxNormColumns) return BSFP8_ERR_UNSUPPORTED;
+    if (!aligned(dweight, 4)) return BSFP8_ERR_INVALID_ARG;
+    if (rows > 0) {
+        if (!dy || !h || !rstd || !dx || ldy < k || ldh < k || ldx < k || (dh && lddh < k)) return BSFP8_ERR_INVALID_ARG;
+        if (!aligned(dy, bytes_of(dy_type)) || !aligned(h, bytes_of(h_type)) || !aligned(dx, bytes_of(h_type)) ||
+            (weight && !aligned(weight, bytes_of(w_type))) || (dh && !aligned(dh, bytes_of(dh_type))) || !aligned(rstd, 4))
+            return BSFP8_ERR_INVALID_ARG;
+        if (dweight && (!workspace || !aligned(workspace, 16) || workspace_bytes < bsfp8::rmsnorm_grad_workspace(rows, k)))
+            return BSFP8_ERR_INVALID_ARG;
+    }
+    return from_hip(bsfp8::launch_rmsnorm_grad(dy, dy_type, ldy, h, h_type, ldh, rstd, weight, w_type, dh, dh_type, lddh,
+                                               rows, k, dx, ldx, dweight, accumulate, workspace, stream));
+}
+
+int64_t block128_grouped_columns(int64_t rows, int64_t groups) {
+    if (rows <= 0 || groups <= 0 || rows > kMaxGroupedRows || groups > bsfp8::groups::kMaxGroups) return 0;
+    return (rows + 127 * std::min(rows, groups)) / 128 * 128;
+}
+
+int64_t block128_grouped_words(int64_t rows, int64_t groups) {
+    if (rows <= 0 || groups <= 0 || rows > kMaxGroupedRows || groups > bsfp8::groups::kMaxGroups) return 0;
+    return rows / 512 + std::min(rows, groups);
+}
+
+bsfp8_status fp8_quantize_grouped_block128(const void* x, bsfp8_out x_type, int64_t source_rows, int64_t k, int64_t ld,
+                                           const int32_t* index, int64_t rows, const int32_t* offsets, int64_t groups,
+                                           bsfp8_format fmt, uint8_t* codes, uint8_t* scales, uint8_t* codes_t,
+                                           int64_t columns, uint8_t* scales_t, int64_t words, hipStream_t stream) {
+    if (!is_fp8(fmt) || !is_element(x_type)) return BSFP8_ERR_UNSUPPORTED;
+    if (rows < 0 || source_rows < 0 || k < 0 || groups < 0 || ld < k || k > kI32Max || source_rows > kI32Max)
+        return BSFP8_ERR_INVALID_ARG;
+    if (rows > kMaxGroupedRows || groups > bsfp8::groups::kMaxGroups) return BSFP8_ERR_UNSUPPORTED;
+    if ((codes == nullptr) != (scales == nullptr) || (codes_t == nullptr) != (scales_t == nullptr))
+        return BSFP8_ERR_INVALID_ARG;
+    if (rows == 0 || k == 0 || groups == 0) return BSFP8_OK;
+    if ((!x && source_rows > 0) || !offsets || (!codes && !codes_t) || (!index && source_rows < rows)) return BSFP8_ERR_INVALID_ARG;
+    if (!aligned(x, bytes_of(x_type)) || !aligned(index, 4) || !aligned(offsets, 4) || !aligned(codes, 16) ||
+        !aligned(codes_t, 16) || !aligned(scales, 4) || !aligned(scales_t, 4))
+        return BSFP8_ERR_INVALID_ARG;
+    if (codes_t) {
+        if (columns % 128 != 0 || columns > kI32Max || columns < block128_grouped_columns(rows, groups) ||
+            words > kI32Max || words < block128_grouped_words(rows, groups))
+            return BSFP8_ERR_INVALID_ARG;
+        if (columns / 128 * ((k + 127) / 128) > kMaxTiles) return BSFP8_ERR_INVALID_ARG;
+    } else if (rows * ((k + 511) / 512) > kMaxRowItems) {
+        return BSFP8_ERR_INVALID_ARG;
+    }
+    return from_hip(bsfp8::launch_quantize_grouped(x, x_type, source_rows, k, ld, index, rows, offsets,
+                                                   static_cast<int>(groups), fmt, codes, scales, codes_t, columns,
+                                                   scales_t, words, stream));
+}
+
+bsfp8_status scaled_gemm_grouped_block128(int64_t M, int64_t N, int64_t K, int64_t groups, const int32_t* offsets,
+                                          bsfp8_format a_fmt, const void* a, const void* a_scales, bsfp8_format b_fmt,
+                                          const void* b, const void* b_scales, int b_block_rows, float alpha,
+                                          const void* c, int64_t ldc, float beta, bsfp8_out out, void* d, int64_t ldd,
+                                          hipStream_t stream) {
+    if (!is_fp8(a_fmt) || !is_fp8(b_fmt) || !is_element(out)) return BSFP8_ERR_UNSUPPORTED;
+    if (b_block_rows != 1 && b_block_rows != 128) return BSFP8_ERR_UNSUPPORTED;
+    if (M < 0 || N < 0 || K < 0 || groups < 0 || (K % 32) != 0) return BSFP8_ERR_INVALID_ARG;
+    if (N > kI32Max - 256 || K > kI32Max) return BSFP8_ERR_INVALID_ARG;
+    if (M > kMaxGroupedRows || groups > bsfp8::groups::kMaxGroups) return BSFP8_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0 || groups == 0) return BSFP8_OK;
+    const uintptr_t es = bytes_of(out);
+    if (!offsets || !aligned(offsets, 4) || !d || ldd < N || !aligned(d, es)) return BSFP8_ERR_INVALID_ARG;
+    if (beta != 0.0f && (!c || ldc < N || !aligned(c, es))) return BSFP8_ERR_INVALID_ARG;
+    if (K > 0 && (!a || !b || !a_scales || !b_scales)) return BSFP8_ERR_INVALID_ARG;
+    if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_scales, 4) || !aligned(b_scales, 4)) return BSFP8_ERR_INVALID_ARG;
+    if (K >= (int64_t(1) << 23)) return BSFP8_ERR_UNSUPPORTED;
+    // a launch's threads are counted in 32 bits
+    if ((N + 15) / 16 * groups > (int64_t(1) << 22) - 1) return BSFP8_ERR_INVALID_ARG;
+    const bsfp8::Epilogue ep{alpha, beta, beta != 0.0f ? c : nullptr, beta != 0.0f ? ldc : 0};
+    const bsfp8::ScaleRows sa{static_cast<const uint32_t*>(a_scales), M, 0};
+    const bsfp8::ScaleRows sb{static_cast<const uint32_t*>(b_scales), b_block_rows == 128 ? (N + 127) / 128 : N,
+                              b_block_rows == 128 ? 7 : 0};
+    return from_hip(bsfp8::launch_gemm_grouped({M, N, K, static_cast<int>(groups), offsets, a_fmt,
+                                                static_cast<const uint8_t*>(a), sa, b_fmt,
+                                                static_cast<const uint8_t*>(b), sb, out, d, ldd, ep, stream}));
+}
+
+bsfp8_status scaled_gemm_grouped_wgrad_block128(int64_t M, int64_t N, int64_t columns, int64_t words, int64_t groups,
+                                                const int32_t* offsets, bsfp8_format a_fmt, const void* a,
+                                                const void* a_scales, bsfp8_format b_fmt, const void* b,
+                                                const void* b_scales, float alpha, const void* c, int64_t ldc,
+                                                int64_t c_group, float beta, bsfp8_out out, void* d, int64_t ldd,
+                                                int64_t d_group, hipStream_t stream) {
+    if (!is_fp8(a_fmt) || !is_fp8(b_fmt) || !is_element(out)) return BSFP8_ERR_UNSUPPORTED;
+    if (M < 0 || N < 0 || columns < 0 || words < 0 || groups < 0 || columns % 128 != 0) return BSFP8_ERR_INVALID_ARG;
+    if (M > kI32Max - 256 || N > kI32Max - 256 || words > kI32Max) return BSFP8_ERR_INVALID_ARG;
+    // the kernels address a 256-row band of an operand with 32-bit offsets
+    if (groups > bsfp8::groups::kMaxGroups || columns >= (int64_t(1) << 23)) return BSFP8_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0 || groups == 0) return BSFP8_OK;
+    const uintptr_t es = bytes_of(out);
+    if (!offsets || !aligned(offsets, 4) || !d || ldd < N || !aligned(d, es)) return BSFP8_ERR_INVALID_ARG;
+    if (groups > 1 && d_group < (M - 1) * ldd + N) return BSFP8_ERR_INVALID_ARG;
+    if (beta != 0.0f && (!c || ldc < N || !aligned(c, es))) return BSFP8_ERR_INVALID_ARG;
+    if (columns > 0 && words > 0 && (!a || !b || !a_scales || !b_scales)) return BSFP8_ERR_INVALID_ARG;
+    if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_scales, 4) || !aligned(b_scales, 4)) return BSFP8_ERR_INVALID_ARG;
+    // a launch's threads are counted in 32 bits
+    if ((M + 31) / 32 * ((N + 31) / 32) > kMaxTiles || (M + 31) / 32 * ((N + 31) / 32) * groups > kMaxTiles)
+        return BSFP8_ERR_INVALID_ARG;
+    const bsfp8::Epilogue ep{alpha, beta, beta != 0.0f ? c : nullptr, beta != 0.0f ? ldc : 0};
+    return from_hip(bsfp8::launch_gemm_grouped_wgrad(
+        {M, N, columns, words, static_cast<int>(groups), offsets, a_fmt, static_cast<const uint8_t*>(a),
+         static_cast<const uint32_t*>(a_scales), b_fmt, static_cast<const uint8_t*>(b),
+         static_cast<const uint32_t*>(b_scales), out, d, ldd, d_group, beta != 0.0f ? c_group : 0, ep, stream}));
+}
+
 bsfp8_status adamw_step(const bsfp8_adamw_tensor* tensors, int64_t count, bsfp8_out p_type, bsfp8_out g_type,
                         bsfp8_state state, const bsfp8_adamw_args* args, hipStream_t stream) {
     if (state != BSFP8_STATE_F32 && state != BSFP8_STATE_FP8) return BSFP8_ERR_UNSUPPORTED;
@@ -429,6 +580,6 @@ const char* bsfp8_status_string(bsfp8_status s) {
     }
 }
 
-int bsfp8_version(void) { return (0 << 16) | 6; }
+int bsfp8_version(void) { return (0 << 16) | 7; }
 
 }  // extern "C"

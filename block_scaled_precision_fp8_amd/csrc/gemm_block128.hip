@@ -21,32 +21,6 @@ namespace bsfp8 {
 namespace {
 
 using namespace big_tile;
-typedef int v8i __attribute__((ext_vector_type(8)));
-
-// acc += x^T y over 64 K values of one scale block; x: row operand (B, scale
-// byte sb), y: column operand (A, scale byte sa), each lane's 32 codes in two
-// quarters.  All 64 K values share the scales, so the order of K within the
-// step is free as long as both operands use the same one.
-template <int AF, int BF, int OUT>
-__device__ __forceinline__ v16f step64(const u32x4& x0, const u32x4& x1, const u32x4& y0, const u32x4& y1,
-                                       uint32_t sb, uint32_t sa, v16f acc) {
-    if constexpr (OUT != BSFP8_OUT_F32) {
-        const v8i x = {(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
-        const v8i y = {(int)y0[0], (int)y0[1], (int)y0[2], (int)y0[3], (int)y1[0], (int)y1[1], (int)y1[2], (int)y1[3]};
-        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, acc, mfma_fmt<BF>(), mfma_fmt<AF>(), 0,
-                                                               static_cast<int>(sb), 0, static_cast<int>(sa));
-    } else {
-        const float fb = __uint_as_float(sb << 23), fa = __uint_as_float(sa << 23);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const u32x4& xs = q < 2 ? x0 : x1;
-            const u32x4& ys = q < 2 ? y0 : y1;
-            acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen8<BF>(xs[2 * (q & 1)], xs[2 * (q & 1) + 1], fb),
-                                                          widen8<AF>(ys[2 * (q & 1)], ys[2 * (q & 1) + 1], fa), acc, 0, 0, 0);
-        }
-        return acc;
-    }
-}
 
 // Narrow form: one workgroup per 32 x 32 output tile, its four waves taking
 // contiguous ranges of the K blocks.  Each load instruction reads whole

@@ -24,34 +24,7 @@ namespace bsfp8 {
 namespace {
 
 using namespace big_tile;
-typedef float v4f __attribute__((ext_vector_type(4)));
-typedef int v8i __attribute__((ext_vector_type(8)));
-
 constexpr int kMaxWaves = 16;
-
-// acc += x^T y over one K block, byte J of the scale words; x: rows of B.
-template <int AF, int BF, int OUT, int J>
-__device__ __forceinline__ v4f block_product(const u32x4& x0, const u32x4& x1, const u32x4& y0, const u32x4& y1,
-                                             uint32_t sb, uint32_t sa, v4f acc) {
-    if constexpr (OUT != BSFP8_OUT_F32) {
-        const v8i x = {(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
-        const v8i y = {(int)y0[0], (int)y0[1], (int)y0[2], (int)y0[3], (int)y1[0], (int)y1[1], (int)y1[2], (int)y1[3]};
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, mfma_fmt<BF>(), mfma_fmt<AF>(), J,
-                                                                static_cast<int>(sb), J, static_cast<int>(sa));
-    } else {
-        const float fb = __uint_as_float(((sb >> (8 * J)) & 255u) << 23), fa = __uint_as_float(((sa >> (8 * J)) & 255u) << 23);
-        typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const u32x4& xs = q < 2 ? x0 : x1;
-            const u32x4& ys = q < 2 ? y0 : y1;
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf8v, widen8<BF>(xs[2 * (q & 1)], xs[2 * (q & 1) + 1], fb)),
-                __builtin_bit_cast(bf8v, widen8<AF>(ys[2 * (q & 1)], ys[2 * (q & 1) + 1], fa)), acc, 0, 0, 0);
-        }
-        return acc;
-    }
-}
 
 template <int AF, int BF, int OUT>
 __global__ __launch_bounds__(64 * kMaxWaves) void gemm_block128_rows_kernel(

@@ -114,6 +114,22 @@ hipError_t launch_gemm_block128(int64_t M, int64_t N, int64_t K, int a_fmt, cons
                                 int a_block_rows, int b_fmt, const uint8_t* b, const uint8_t* b_scales,
                                 int b_block_rows, int out, void* d, int64_t ldd, const Epilogue& ep,
                                 hipStream_t stream);
+// The norm of x (+ residual), to FP8 codes and to y; outputs that are null are not wanted.
+hipError_t launch_rmsnorm(const void* x, int x_type, int64_t rows, int64_t k, int64_t ldx, const void* residual,
+                          int h_type, int64_t ldr, const void* weight, int w_type, float eps, int fmt, uint8_t* codes,
+                          uint8_t* scales, void* y, int y_type, int64_t ldy, void* h, int64_t ldh, float* rstd,
+                          hipStream_t stream);
+// Its gradients; dweight null: not wanted, and the workspace not used.
+int64_t rmsnorm_grad_workspace(int64_t rows, int64_t k);
+hipError_t launch_rmsnorm_grad(const void* dy, int dy_type, int64_t ldy, const void* h, int h_type, int64_t ldh,
+                               const float* rstd, const void* weight, int w_type, const void* dh, int dh_type,
+                               int64_t lda, int64_t rows, int64_t k, void* dx, int64_t ldx, float* dweight,
+                               int accumulate, void* workspace, hipStream_t stream);
+// launch_quantize_block128 with 1 x 128 blocks of rows in groups, taken by index (or in place, null).
+hipError_t launch_quantize_grouped(const void* x, int x_type, int64_t source, int64_t k, int64_t ld,
+                                   const int32_t* index, int64_t rows, const int32_t* offsets, int groups, int fmt,
+                                   uint8_t* codes, uint8_t* scales, uint8_t* codes_t, int64_t columns,
+                                   uint8_t* scales_t, int64_t words, hipStream_t stream);
 // One AdamW step over count tensors (checked by the API layer).
 hipError_t launch_adamw(const bsfp8_adamw_tensor* tensors, int64_t count, int p_type, int g_type, int state,
                         const bsfp8_adamw_args& args, hipStream_t stream);

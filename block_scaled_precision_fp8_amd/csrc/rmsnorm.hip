@@ -1,0 +1,444 @@
+// rmsnorm.hip -- root-mean-square norm with the residual's addition, to FP8 codes with
+// one power-of-two scale per 1 x 128 block and to 16 or 32 bits, and its gradient (gfx950).
+//
+//   h = x + residual, rounded to the residual's type     rstd = (mean_k h^2 + eps)^(-1/2)
+//   y = (h rstd) w                                       codes and scales: those of y
+//
+// The norm is taken of the rounded h, the values that a later backward pass reads, so that
+// the gradient is that of the function that ran.  y stays in FP32 until it is encoded
+// or converted: each output is rounded once.  With g = w dy, xh = h rstd:
+//
+//   dx = rstd (g - xh mean_k(g xh)) + dh                 dw = sum_rows dy xh
+//
+// dh being the gradient that reaches h along the residual.  Sums are FP32: a lane's
+// columns in order, then across lanes, then across waves, in a fixed order.
+//
+// A row is held in registers between its two passes, so each input is read once: HBM
+// bounds the large calls.  Waves take 512 columns at a time, eight per lane: four blocks of
+// 128 (16 lanes each) are one word of scale bytes, and a lane's eight codes one 8-byte store.
+#include "block128_codec.h"
+
+namespace bsfp8 {
+
+namespace {
+
+using namespace block128;
+
+constexpr int kWaveColumns = 512;
+constexpr int kMaxWaves = 16;
+typedef u4v u4u __attribute__((aligned(2)));     // 16 bytes at any element's address
+enum { NONE = 0, HALF = 1, WIDE = 2 };           // absent, a 16-bit type, FP32
+
+// Eight elements of a row as loaded.
+template <int W>
+struct Raw { u4v w[W == WIDE ? 2 : 1]; };
+
+// Elements at .. at + 7 of p, of which n (or all) exist; zeros for the others.
+template <int W>
+__device__ __forceinline__ Raw<W> load_raw(const void* p, int64_t at, int64_t n) {
+    Raw<W> r;
+    if constexpr (W == WIDE) {
+        const uint32_t* q = static_cast<const uint32_t*>(p) + at;
+        if (n >= 8) {
+            r.w[0] = __builtin_nontemporal_load(reinterpret_cast<const u4u*>(q));
+            r.w[1] = __builtin_nontemporal_load(reinterpret_cast<const u4u*>(q + 4));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r.w[j >> 2][j & 3] = j < n ? q[j] : 0u;
+        }
+    } else {
+        const uint16_t* q = static_cast<const uint16_t*>(p) + at;
+        if (n >= 8) {
+            r.w[0] = __builtin_nontemporal_load(reinterpret_cast<const u4u*>(q));
+        } else {
+            r.w[0] = u4v{0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n) r.w[0][j >> 1] |= static_cast<uint32_t>(q[j]) << (16 * (j & 1));
+        }
+    }
+    return r;
+}
+template <int T>
+__device__ __forceinline__ void half_values(const u4v& w, float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = from_half_bits<T>(static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1))));
+}
+template <int W>
+__device__ __forceinline__ void values(const Raw<W>& r, int type, float (&v)[8]) {
+    if constexpr (W == WIDE) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r.w[j >> 2][j & 3]);
+    } else if (type == BSFP8_OUT_BF16) {
+        half_values<BSFP8_OUT_BF16>(r.w[0], v);
+    } else {
+        half_values<BSFP8_OUT_F16>(r.w[0], v);
+    }
+}
+template <int T>
+__device__ __forceinline__ u4v half_words(const float (&v)[8]) {
+    u4v w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        w[j] = to_half_bits<T>(v[2 * j]) | (static_cast<uint32_t>(to_half_bits<T>(v[2 * j + 1])) << 16);
+    return w;
+}
+template <int W>
+__device__ __forceinline__ Raw<W> rounded(const float (&v)[8], int type) {
+    Raw<W> r;
+    if constexpr (W == WIDE) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r.w[j >> 2][j & 3] = __float_as_uint(v[j]);
+    } else if (type == BSFP8_OUT_BF16) {
+        r.w[0] = half_words<BSFP8_OUT_BF16>(v);
+    } else {
+        r.w[0] = half_words<BSFP8_OUT_F16>(v);
+    }
+    return r;
+}
+template <int W>
+__device__ __forceinline__ void store_raw(void* p, int64_t at, int64_t n, const Raw<W>& r) {
+    if constexpr (W == WIDE) {
+        uint32_t* q = static_cast<uint32_t*>(p) + at;
+        if (n >= 8) {
+            *reinterpret_cast<u4u*>(q) = r.w[0];
+            *reinterpret_cast<u4u*>(q + 4) = r.w[1];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n) q[j] = r.w[j >> 2][j & 3];
+        }
+    } else {
+        uint16_t* q = static_cast<uint16_t*>(p) + at;
+        if (n >= 8) {
+            *reinterpret_cast<u4u*>(q) = r.w[0];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n) q[j] = static_cast<uint16_t>(r.w[0][j >> 1] >> (16 * (j & 1)));
+        }
+    }
+}
+// Eight weights (ones without an array), raw: their type is only known here.
+__device__ __forceinline__ Raw<WIDE> load_weight(const void* w, int type, int64_t col, int64_t n) {
+    Raw<WIDE> r;
+    r.w[0] = r.w[1] = u4v{0x3F800000u, 0x3F800000u, 0x3F800000u, 0x3F800000u};
+    if (!w) return r;
+    if (type == BSFP8_OUT_F32) return load_raw<WIDE>(w, col, n);
+    r.w[0] = load_raw<HALF>(w, col, n).w[0];
+    return r;
+}
+__device__ __forceinline__ void weight_values(const Raw<WIDE>& r, bool given, int type, float (&v)[8]) {
+    if (given && type != BSFP8_OUT_F32) values<HALF>(Raw<HALF>{{r.w[0]}}, type, v);
+    else values<WIDE>(r, type, v);
+}
+
+// The sum over a wave, in each of its lanes.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+    return v;
+}
+// The sum over the `group` waves of a row.  One barrier is enough where calls in turn
+// alternate between two arrays `part`.
+__device__ __forceinline__ float row_sum(float v, float* part, int wave, int group) {
+    v = wave_sum(v);
+    if (group == 1) return v;
+    if ((threadIdx.x & 63) == 0) part[wave] = v;
+    __syncthreads();
+    const int first = wave / group * group;
+    v = part[first];
+    for (int i = 1; i < group; ++i) v += part[first + i];
+    return v;
+}
+
+struct NormArgs {
+    const void* x;
+    const void* r;
+    const void* w;
+    uint8_t* codes;
+    uint32_t* scales;
+    void* y;
+    void* h;
+    float* rstd;
+    int64_t rows, k, ldx, ldr, ldy, ldh;
+    int x_type, h_type, w_type, y_type, group;
+    float eps;
+};
+
+// X: x's width, R: the residual's, C: pieces of 512 columns per wave.
+template <int X, int R, int FMT, int C>
+__global__ __launch_bounds__(64 * kMaxWaves) void rmsnorm_kernel(NormArgs a) {
+    __shared__ float part[2][kMaxWaves];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int per = (blockDim.x >> 6) / a.group;     // rows at once
+    const int64_t kp = (a.k + 31) & ~static_cast<int64_t>(31);
+    const int w0 = wave % a.group;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * per;
+    int turn = 0;
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * per; base < a.rows; base += step, turn ^= 1) {
+        const int64_t row = base + wave / a.group;
+        const bool in = row < a.rows;
+        Raw<X> xr[C];
+        Raw<R> rr[C];
+        Raw<WIDE> wr[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int64_t col = static_cast<int64_t>(c * a.group + w0) * kWaveColumns + 8 * lane;
+            const int64_t n = in ? a.k - col : 0;
+            xr[c] = load_raw<X>(a.x, row * a.ldx + col, n);
+            if constexpr (R != NONE) rr[c] = load_raw<R>(a.r, row * a.ldr + col, n);
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int64_t col = static_cast<int64_t>(c * a.group + w0) * kWaveColumns + 8 * lane;
+            wr[c] = load_weight(a.w, a.w_type, col, a.k - col);
+        }
+        float h[C][8];
+        float sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int64_t col = static_cast<int64_t>(c * a.group + w0) * kWaveColumns + 8 * lane;
+            values<X>(xr[c], a.x_type, h[c]);
+            if constexpr (R != NONE) {
+                float q[8];
+                values<R>(rr[c], a.h_type, q);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[c][j] += q[j];
+                const Raw<R> hr = rounded<R>(h[c], a.h_type);
+                values<R>(hr, a.h_type, h[c]);
+                if (in) store_raw<R>(a.h, row * a.ldh + col, a.k - col, hr);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum = fmaf(h[c][j], h[c][j], sum);
+        }
+        sum = row_sum(sum, part[turn], wave, a.group);
+        if (!in) continue;
+        const float rstd = 1.0f / sqrtf(sum / static_cast<float>(a.k) + a.eps);
+        if (a.rstd && w0 == 0 && lane == 0) a.rstd[row] = rstd;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int g = c * a.group + w0;
+            const int64_t col = static_cast<int64_t>(g) * kWaveColumns + 8 * lane;
+            if (static_cast<int64_t>(g) * kWaveColumns >= a.k) break;
+            float w[8], y[8];
+            weight_values(wr[c], a.w != nullptr, a.w_type, w);
+            // (columns past k: zeros, whatever rstd is)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = col + j < a.k ? (h[c][j] * rstd) * w[j] : 0.0f;
+            if (a.y) {
+                if (a.y_type == BSFP8_OUT_F32) store_raw<WIDE>(a.y, row * a.ldy + col, a.k - col, rounded<WIDE>(y, a.y_type));
+                else store_raw<HALF>(a.y, row * a.ldy + col, a.k - col, rounded<HALF>(y, a.y_type));
+            }
+            if (a.codes) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m = umax(m, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+                const uint32_t byte = scale_byte<FMT>(max16(m));
+                const float f = inverse_scale(byte);
+                uint32_t c0 = fp8_pack4<FMT>(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
+                uint32_t c1 = fp8_pack4<FMT>(y[4] * f, y[5] * f, y[6] * f, y[7] * f);
+                if (byte == 255u) c0 = c1 = kNanCodes;
+                if (col < kp) *reinterpret_cast<uint2*>(a.codes + row * kp + col) = make_uint2(c0, c1);
+                const uint32_t word = __builtin_amdgcn_readlane(byte, 0) | (__builtin_amdgcn_readlane(byte, 16) << 8) |
+                                      (__builtin_amdgcn_readlane(byte, 32) << 16) | (__builtin_amdgcn_readlane(byte, 48) << 24);
+                if (lane == 0) a.scales[g * a.rows + row] = word;
+            }
+        }
+    }
+}
+
+struct GradArgs {
+    const void* dy;
+    const void* h;
+    const float* rstd;
+    const void* w;
+    const void* dh;
+    void* dx;
+    float* partial;              // null: the weight's gradient is not wanted
+    int64_t rows, k, ldy, ldh, lda, ldx;
+    int dy_type, h_type, w_type, dh_type, group;
+};
+
+// Y: dy's width, H: h's and dx's, A: dh's.
+template <int Y, int H, int A, int C>
+__global__ __launch_bounds__(64 * kMaxWaves) void rmsnorm_grad_kernel(GradArgs a) {
+    __shared__ float part[2][kMaxWaves];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int per = (blockDim.x >> 6) / a.group;
+    const int w0 = wave % a.group;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * per;
+    float acc[C][8] = {};
+    int turn = 0;
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * per; base < a.rows; base += step, turn ^= 1) {
+        const int64_t row = base + wave / a.group;
+        const bool in = row < a.rows;
+        Raw<Y> yr[C];
+        Raw<H> hr[C];
+        Raw<A> ar[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int64_t col = static_cast<int64_t>(c * a.group + w0) * kWaveColumns + 8 * lane;
+            const int64_t n = in ? a.k - col : 0;
+            yr[c] = load_raw<Y>(a.dy, row * a.ldy + col, n);
+            hr[c] = load_raw<H>(a.h, row * a.ldh + col, n);
+            if constexpr (A != NONE) ar[c] = load_raw<A>(a.dh, row * a.lda + col, n);
+        }
+        const float rstd = in ? a.rstd[row] : 0.0f;
+        float sum = 0.0f;
+        float g[C][8], xh[C][8];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int64_t col = static_cast<int64_t>(c * a.group + w0) * kWaveColumns + 8 * lane;
+            float w[8];
+            weight_values(load_weight(a.w, a.w_type, col, a.k - col), a.w != nullptr, a.w_type, w);
+            values<Y>(yr[c], a.dy_type, g[c]);
+            values<H>(hr[c], a.h_type, xh[c]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                // (columns past k: zeros, whatever rstd is)
+                xh[c][j] = col + j < a.k ? xh[c][j] * rstd : 0.0f;
+                if (in) acc[c][j] = fmaf(g[c][j], xh[c][j], acc[c][j]);
+                g[c][j] = col + j < a.k ? g[c][j] * w[j] : 0.0f;
+                sum = fmaf(g[c][j], xh[c][j], sum);
+            }
+        }
+        sum = row_sum(sum, part[turn], wave, a.group);
+        if (!in) continue;
+        const float mean = sum / static_cast<float>(a.k);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int64_t col = static_cast<int64_t>(c * a.group + w0) * kWaveColumns + 8 * lane;
+            float dx[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dx[j] = rstd * fmaf(-xh[c][j], mean, g[c][j]);
+            if constexpr (A != NONE) {
+                float q[8];
+                values<A>(ar[c], a.dh_type, q);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dx[j] += q[j];
+            }
+            store_raw<H>(a.dx, row * a.ldx + col, a.k - col, rounded<H>(dx, a.h_type));
+        }
+    }
+    if (!a.partial) return;
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * per + wave / a.group) * a.k;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int64_t col = static_cast<int64_t>(c * a.group + w0) * kWaveColumns + 8 * lane;
+        store_raw<WIDE>(a.partial, at + col, a.k - col, rounded<WIDE>(acc[c], BSFP8_OUT_F32));
+    }
+}
+
+// dw[c] (+)= the sum of `count` partial rows: 64 columns per workgroup, its waves
+// taking every 16th row, their sums added in order.
+__global__ __launch_bounds__(64 * kMaxWaves) void column_sum_kernel(const float* __restrict__ partial, int64_t count,
+                                                                    int64_t k, int accumulate, float* __restrict__ dw) {
+    __shared__ float part[kMaxWaves][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+    float sum = 0.0f;
+    if (col < k)
+        for (int64_t r = wave; r < count; r += kMaxWaves) sum += partial[r * k + col];
+    part[wave][lane] = sum;
+    __syncthreads();
+    if (wave != 0 || col >= k) return;
+    for (int w = 1; w < kMaxWaves; ++w) sum += part[w][lane];
+    dw[col] = accumulate ? dw[col] + sum : sum;
+}
+
+// How a row is spread: `pieces` of 512 columns per wave, `group` waves per row, `per`
+// rows per workgroup at once, `grid` workgroups.
+struct Spread { int pieces, group, per, grid; };
+
+Spread norm_spread(int64_t rows, int64_t k) {
+    const int n = static_cast<int>((k + kWaveColumns - 1) / kWaveColumns);
+    const int pieces = n <= 4 || (n <= kMaxWaves && rows <= 512) ? 1 : n <= 2 * kMaxWaves ? 2 : 4;
+    const int group = (n + pieces - 1) / pieces, per = group >= 4 ? 1 : 4 / group;
+    const int64_t grid = (rows + per - 1) / per;
+    return {pieces, group, per, static_cast<int>(grid < (1 << 20) ? grid : 1 << 20)};
+}
+
+Spread grad_spread(int64_t rows, int64_t k) {
+    const int n = static_cast<int>((k + kWaveColumns - 1) / kWaveColumns);
+    const int pieces = n <= 4 ? 1 : n <= 2 * kMaxWaves ? 2 : 4;
+    const int group = (n + pieces - 1) / pieces, per = group >= 4 ? 1 : 4 / group;
+    const int64_t grid = (rows + per - 1) / per, most = 512;
+    return {pieces, group, per, static_cast<int>(grid < most ? grid : most)};
+}
+
+template <int X, int R, int FMT>
+hipError_t launch_norm(const NormArgs& a, const Spread& s, hipStream_t stream) {
+    const dim3 grid(s.grid), threads(64 * s.group * s.per);
+    if (s.pieces == 1) hipLaunchKernelGGL((rmsnorm_kernel<X, R, FMT, 1>), grid, threads, 0, stream, a);
+    else if (s.pieces == 2) hipLaunchKernelGGL((rmsnorm_kernel<X, R, FMT, 2>), grid, threads, 0, stream, a);
+    else hipLaunchKernelGGL((rmsnorm_kernel<X, R, FMT, 4>), grid, threads, 0, stream, a);
+    return hipGetLastError();
+}
+
+template <int X, int R>
+hipError_t launch_norm_fmt(const NormArgs& a, int fmt, const Spread& s, hipStream_t stream) {
+    return fmt == BSFP8_E4M3 ? launch_norm<X, R, BSFP8_E4M3>(a, s, stream) : launch_norm<X, R, BSFP8_E5M2>(a, s, stream);
+}
+
+template <int Y, int H, int A>
+hipError_t launch_grad(const GradArgs& a, const Spread& s, hipStream_t stream) {
+    const dim3 grid(s.grid), threads(64 * s.group * s.per);
+    if (s.pieces == 1) hipLaunchKernelGGL((rmsnorm_grad_kernel<Y, H, A, 1>), grid, threads, 0, stream, a);
+    else if (s.pieces == 2) hipLaunchKernelGGL((rmsnorm_grad_kernel<Y, H, A, 2>), grid, threads, 0, stream, a);
+    else hipLaunchKernelGGL((rmsnorm_grad_kernel<Y, H, A, 4>), grid, threads, 0, stream, a);
+    return hipGetLastError();
+}
+
+template <int Y, int H>
+hipError_t launch_grad_dh(const GradArgs& a, const Spread& s, hipStream_t stream) {
+    if (!a.dh) return launch_grad<Y, H, NONE>(a, s, stream);
+    return a.dh_type == BSFP8_OUT_F32 ? launch_grad<Y, H, WIDE>(a, s, stream) : launch_grad<Y, H, HALF>(a, s, stream);
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const void* x, int x_type, int64_t rows, int64_t k, int64_t ldx, const void* residual,
+                          int h_type, int64_t ldr, const void* weight, int w_type, float eps, int fmt, uint8_t* codes,
+                          uint8_t* scales, void* y, int y_type, int64_t ldy, void* h, int64_t ldh, float* rstd,
+                          hipStream_t stream) {
+    const Spread s = norm_spread(rows, k);
+    const NormArgs a{x, residual, weight, codes, reinterpret_cast<uint32_t*>(scales), y, h, rstd, rows, k, ldx, ldr,
+                     ldy, ldh, x_type, h_type, w_type, y_type, s.group, eps};
+    if (x_type == BSFP8_OUT_F32) {
+        if (!residual) return launch_norm_fmt<WIDE, NONE>(a, fmt, s, stream);
+        return h_type == BSFP8_OUT_F32 ? launch_norm_fmt<WIDE, WIDE>(a, fmt, s, stream)
+                                       : launch_norm_fmt<WIDE, HALF>(a, fmt, s, stream);
+    }
+    if (!residual) return launch_norm_fmt<HALF, NONE>(a, fmt, s, stream);
+    return h_type == BSFP8_OUT_F32 ? launch_norm_fmt<HALF, WIDE>(a, fmt, s, stream)
+                                   : launch_norm_fmt<HALF, HALF>(a, fmt, s, stream);
+}
+
+int64_t rmsnorm_grad_workspace(int64_t rows, int64_t k) {
+    const Spread s = grad_spread(rows, k);
+    return static_cast<int64_t>(s.grid) * s.per * k * 4;
+}
+
+hipError_t launch_rmsnorm_grad(const void* dy, int dy_type, int64_t ldy, const void* h, int h_type, int64_t ldh,
+                               const float* rstd, const void* weight, int w_type, const void* dh, int dh_type,
+                               int64_t lda, int64_t rows, int64_t k, void* dx, int64_t ldx, float* dweight,
+                               int accumulate, void* workspace, hipStream_t stream) {
+    const Spread s = grad_spread(rows, k);
+    const GradArgs a{dy, h, rstd, weight, dh, dx, dweight ? static_cast<float*>(workspace) : nullptr, rows, k, ldy,
+                     ldh, lda, ldx, dy_type, h_type, w_type, dh_type, s.group};
+    hipError_t e = hipSuccess;
+    if (rows == 0) e = hipSuccess;                   // only the weight's gradient: zeros
+    else if (dy_type == BSFP8_OUT_F32)
+        e = h_type == BSFP8_OUT_F32 ? launch_grad_dh<WIDE, WIDE>(a, s, stream) : launch_grad_dh<WIDE, HALF>(a, s, stream);
+    else
+        e = h_type == BSFP8_OUT_F32 ? launch_grad_dh<HALF, WIDE>(a, s, stream) : launch_grad_dh<HALF, HALF>(a, s, stream);
+    if (e != hipSuccess || !dweight) return e;
+    hipLaunchKernelGGL(column_sum_kernel, dim3(static_cast<uint32_t>((k + 63) / 64)), dim3(64 * kMaxWaves), 0, stream,
+                       a.partial, static_cast<int64_t>(s.grid) * s.per, k, accumulate, dweight);
+    return hipGetLastError();
+}
+
+}  // namespace bsfp8

@@ -427,6 +427,132 @@ bsfp8_status scaled_gemm_block128(int64_t M, int64_t N, int64_t K, bsfp8_format 
                                   hipStream_t stream);
 
 /*
+ * rmsnorm_quantize_block128 -- the residual's addition and root-mean-square norm ahead of a
+ * projection, to FP8 codes with one E8M0 scale per 1 x 128 block, from one read.
+ *
+ *   h = x + residual, rounded to h_type (without a residual h = x)
+ *   rstd = 1 / sqrt(mean over k of h^2 + eps)          y = (h * rstd) * weight
+ *
+ * x:        rows x k elements of x_type, row-major, leading dimension ldx >= k.
+ * residual: NULL, or rows x k of h_type (ldr); then h receives the sum (rows x k of
+ *           h_type, ldh).  h may be residual itself, or x itself where the types agree.
+ * weight:   NULL (ones), or k elements of w_type.
+ * eps:      finite, >= 0.
+ * codes, scales: out, as fp8_quantize_block128 with block_rows 1 writes them for the
+ *           FP32 matrix y; both NULL: not wanted.
+ * y:        out, rows x k of y_type (ldy), rounded once from FP32; NULL: not wanted.
+ *           codes or y must be given.  y may be x itself where the types agree.
+ * rstd:     out, FP32 [rows], what rmsnorm_backward takes; NULL: not wanted.
+ * rows >= 0; k at most 32768 (BSFP8_ERR_UNSUPPORTED beyond).  Every array is aligned to
+ * its element size, codes to 16 bytes, scales to 4; any other overlap is undefined.
+ *
+ * FP32 arithmetic, each operation rounded once; the sum of squares in a fixed order, so
+ * equal calls give equal bits.  The norm is that of the rounded h, which a backward
+ * pass reads.  Infinities and NaN spread as the formulas have it: a NaN to its row,
+ * an infinity (rstd = 0) to itself as NaN, its row otherwise zeros.  Blocks of y with a
+ * non-finite value get the scale byte 255 and NaN codes.  rows == 0 or k == 0 writes nothing.
+ */
+bsfp8_status rmsnorm_quantize_block128(const void* x, bsfp8_out x_type, int64_t rows, int64_t k, int64_t ldx,
+                                       const void* residual, bsfp8_out h_type, int64_t ldr, const void* weight,
+                                       bsfp8_out w_type, float eps, bsfp8_format fmt, uint8_t* codes, uint8_t* scales,
+                                       void* y, bsfp8_out y_type, int64_t ldy, void* h, int64_t ldh, float* rstd,
+                                       hipStream_t stream);
+
+/*
+ * rmsnorm_backward -- the gradients of y = (h * rstd(h)) * weight.
+ *
+ *   g = dy * weight, xh = h * rstd
+ *   dx = rstd (g - xh mean(g xh)) (+ dh)               dweight = sum over rows of dy xh
+ *
+ * dy: rows x k of dy_type (ldy); h: rows x k of h_type (ldh) and rstd as the forward call
+ * left them; weight as there.  dh: NULL, or the gradient that reaches h along the
+ * residual, rows x k of dh_type (lddh).  dx: out, rows x k of h_type (ldx), the
+ * gradient of x and of the residual; it may be dy, h or dh itself where type and leading
+ * dimension agree.  dweight: out, FP32 [k], added to what is there with accumulate = 1
+ * (0 otherwise); NULL: not wanted.  workspace: rmsnorm_backward_workspace(rows, k) bytes,
+ * 16-byte aligned (needed with dweight only); calls that may run at once need one each.
+ * FP32 arithmetic, sums in a fixed order.  rows == 0 writes only dweight (zeros, or
+ * nothing with accumulate); k as in the forward call.
+ */
+int64_t rmsnorm_backward_workspace(int64_t rows, int64_t k);
+bsfp8_status rmsnorm_backward(const void* dy, bsfp8_out dy_type, int64_t ldy, const void* h, bsfp8_out h_type,
+                              int64_t ldh, const float* rstd, const void* weight, bsfp8_out w_type, const void* dh,
+                              bsfp8_out dh_type, int64_t lddh, int64_t rows, int64_t k, void* dx, int64_t ldx,
+                              float* dweight, int accumulate, void* workspace, int64_t workspace_bytes,
+                              hipStream_t stream);
+
+/*
+ * Grouped operators: rows sorted by group (by the expert a token is sent to), group e
+ * being rows offsets[e] .. offsets[e + 1] - 1.  offsets is a DEVICE array of
+ * groups + 1 int32 that does not decrease, from >= 0 to <= rows; it is read when the kernels run,
+ * so that no size has to reach the host and a captured call follows it.  Groups may be
+ * empty; rows of no group are left as they were.  An array that breaks these rules gives
+ * undefined results within the outputs, never an access outside the arrays.  At most
+ * 1024 groups and 2^30 rows (BSFP8_ERR_UNSUPPORTED beyond).
+ */
+
+/*
+ * fp8_quantize_grouped_block128 -- fp8_quantize_block128 (1 x 128 blocks) of rows in
+ * groups, optionally taken by index, and of their transpose group by group.
+ *
+ * x:      source_rows x k of x_type, leading dimension ld, as fp8_quantize_block128.
+ * index:  NULL (then source_rows >= rows), or a device array of `rows` int32: sorted row i
+ *         is row index[i] of x; a number outside 0 .. source_rows - 1 stands for a row of zeros.
+ * codes, scales: out, those of the sorted rows (rows x kp, [ceil(k / 512)][rows][4]);
+ *         both NULL: not wanted.
+ * codes_t, scales_t: out, those of the transpose; both NULL: not wanted.  codes_t is k rows of
+ *         `columns` bytes: group e's rows are the columns from c(e) on, c(e) the sum of
+ *         the sizes before it, each rounded up to a multiple of 128; zero codes fill
+ *         its last block (NaN codes where the block holds an infinity or a NaN).
+ *         scales_t is [words][k][4]: group e's words start at w(e), the sum over the
+ *         groups before it of ceil(size / 512); byte (w(e) + j / 4, r, j % 4) is the scale of its
+ *         block j of row r, unused bytes of its last word 127.  What lies past the last
+ *         group is left as it was.
+ * columns, words: a multiple of 128 and a count, at least what
+ *         block128_grouped_columns(rows, groups) and block128_grouped_words(rows, groups) return
+ *         (enough for any sizes of so many groups).
+ */
+int64_t block128_grouped_columns(int64_t rows, int64_t groups);
+int64_t block128_grouped_words(int64_t rows, int64_t groups);
+bsfp8_status fp8_quantize_grouped_block128(const void* x, bsfp8_out x_type, int64_t source_rows, int64_t k, int64_t ld,
+                                           const int32_t* index, int64_t rows, const int32_t* offsets, int64_t groups,
+                                           bsfp8_format fmt, uint8_t* codes, uint8_t* scales, uint8_t* codes_t,
+                                           int64_t columns, uint8_t* scales_t, int64_t words, hipStream_t stream);
+
+/*
+ * scaled_gemm_grouped_block128 -- D[i] = alpha deq(A)[i] deq(B[e])^T + beta C[i] for the rows i of
+ * each group e: the forward product of experts and, with transposed weights, the gradient
+ * of their input.
+ *
+ * a: M x K codes, a_scales E8M0 words [ceil(K / 512)][M][4] (1 x 128 blocks); b: `groups`
+ * matrices of N x K codes, one after another, b_scales likewise [groups][ceil(K / 512)][R][4], R = N or
+ * ceil(N / 128) for b_block_rows 1 or 128.  alpha, c, ldc, beta, out, d, ldd, the
+ * limits on N and K and the accuracy: as for scaled_gemm_block128.
+ */
+bsfp8_status scaled_gemm_grouped_block128(int64_t M, int64_t N, int64_t K, int64_t groups, const int32_t* offsets,
+                                          bsfp8_format a_fmt, const void* a, const void* a_scales, bsfp8_format b_fmt,
+                                          const void* b, const void* b_scales, int b_block_rows, float alpha,
+                                          const void* c, int64_t ldc, float beta, bsfp8_out out, void* d, int64_t ldd,
+                                          hipStream_t stream);
+
+/*
+ * scaled_gemm_grouped_wgrad_block128 -- D[e] = alpha sum over the rows i of group e of
+ * deq(A)[:, i] deq(B)[:, i]^T + beta C[e]: the weight gradients of experts.
+ *
+ * a: M x columns, b: N x columns codes, a_scales [words][M][4], b_scales [words][N][4]:
+ * transposes that fp8_quantize_grouped_block128 wrote with the same offsets.  columns below 2^23
+ * (BSFP8_ERR_UNSUPPORTED).  d: `groups` matrices of M x N, d_group elements apart (at least
+ * (M - 1) ldd + N with more than one group), c likewise (c_group).  A group without
+ * rows gives beta C (zeros for beta == 0).  Otherwise as scaled_gemm_block128.
+ */
+bsfp8_status scaled_gemm_grouped_wgrad_block128(int64_t M, int64_t N, int64_t columns, int64_t words, int64_t groups,
+                                                const int32_t* offsets, bsfp8_format a_fmt, const void* a,
+                                                const void* a_scales, bsfp8_format b_fmt, const void* b,
+                                                const void* b_scales, float alpha, const void* c, int64_t ldc,
+                                                int64_t c_group, float beta, bsfp8_out out, void* d, int64_t ldd,
+                                                int64_t d_group, hipStream_t stream);
+
+/*
  * The states of an AdamW step: FP32, or FP8 (E4M3 codes with one E8M0 scale
  * per 128 consecutive elements).
  */
