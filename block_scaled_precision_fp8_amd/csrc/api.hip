@@ -446,8 +446,8 @@ bsfp8_status scaled_gemm_grouped_block128(int64_t M, int64_t N, int64_t K, int64
     if (K > 0 && (!a || !b || !a_scales || !b_scales)) return BSFP8_ERR_INVALID_ARG;
     if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_scales, 4) || !aligned(b_scales, 4)) return BSFP8_ERR_INVALID_ARG;
     if (K >= (int64_t(1) << 23)) return BSFP8_ERR_UNSUPPORTED;
-    // a launch's threads are counted in 32 bits
-    if ((N + 15) / 16 * groups > (int64_t(1) << 22) - 1) return BSFP8_ERR_INVALID_ARG;
+    // tiles of 64 x 128, at most: a launch's threads are counted in 32 bits
+    if ((M / 64 + groups) * ((N + 127) / 128) > 2 * kMaxTiles - 16) return BSFP8_ERR_INVALID_ARG;
     const bsfp8::Epilogue ep{alpha, beta, beta != 0.0f ? c : nullptr, beta != 0.0f ? ldc : 0};
     const bsfp8::ScaleRows sa{static_cast<const uint32_t*>(a_scales), M, 0};
     const bsfp8::ScaleRows sb{static_cast<const uint32_t*>(b_scales), b_block_rows == 128 ? (N + 127) / 128 : N,
@@ -475,8 +475,8 @@ bsfp8_status scaled_gemm_grouped_wgrad_block128(int64_t M, int64_t N, int64_t co
     if (beta != 0.0f && (!c || ldc < N || !aligned(c, es))) return BSFP8_ERR_INVALID_ARG;
     if (columns > 0 && words > 0 && (!a || !b || !a_scales || !b_scales)) return BSFP8_ERR_INVALID_ARG;
     if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_scales, 4) || !aligned(b_scales, 4)) return BSFP8_ERR_INVALID_ARG;
-    // a launch's threads are counted in 32 bits
-    if ((M + 31) / 32 * ((N + 31) / 32) > kMaxTiles || (M + 31) / 32 * ((N + 31) / 32) * groups > kMaxTiles)
+    // tiles of 128 x 128, padded to 8 for each group
+    if ((M + 127) / 128 * ((N + 127) / 128) > kMaxTiles || ((M + 127) / 128 * ((N + 127) / 128) + 7) * groups > kMaxTiles)
         return BSFP8_ERR_INVALID_ARG;
     const bsfp8::Epilogue ep{alpha, beta, beta != 0.0f ? c : nullptr, beta != 0.0f ? ldc : 0};
     return from_hip(bsfp8::launch_gemm_grouped_wgrad(

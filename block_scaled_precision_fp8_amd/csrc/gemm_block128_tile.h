@@ -34,7 +34,7 @@
 // and written, so only the first tile of a workgroup waits for memory.
 #pragma once
 
-#include "gemm_block128.h"
+#include "gemm_grouped.h"
 
 namespace bsfp8 {
 
@@ -83,6 +83,12 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, b2));
 }
 
+template <int OUT>
+__device__ __forceinline__ uint32_t half_pair(float a, float b) {
+    if constexpr (OUT == BSFP8_OUT_BF16) return bf16_pair(a, b);
+    else return to_half_bits<OUT>(a) | (static_cast<uint32_t>(to_half_bits<OUT>(b)) << 16);
+}
+
 template <int TA, int TB>
 struct Tile {
     static constexpr int ROWS_A = 64 * TA, ROWS_B = 64 * TB;
@@ -111,16 +117,39 @@ struct Tile {
     static constexpr int STORES = TA * TB * 2;                      // of the constant-count epilogue
 };
 
+// What a kernel's tiles are tiles of: one product; one product per group of rows
+// (D[i] = A[i] B[e]^T); or one per group of K values (D[e] = A[:, i] B[:, i]^T over group e's i).
+enum Kind { ONE, ROWS, COLUMNS };
+// Where the groups' kernels keep what they read off the offsets: for ROWS a group's first row
+// and first tile, for COLUMNS its first K block and first scale word, and their ends.  (Static, of
+// the most groups: sized at the launch, it made the 256 x 256 tiles take half an hour to compile.)
+struct Tables { int32_t at[groups::kMaxGroups + 1], of[groups::kMaxGroups + 1]; };
+struct GroupsArg {
+    const int32_t* offsets;
+    int count;
+    int64_t words, d_group, c_group;
+};
+
 // FAST: bf16 output, alpha = 1, without C, every chunk of 8 outputs whole and aligned: the
 // epilogue is then a fixed number of range-checked buffer stores, so the loop
 // can leave them in flight.
-template <int AF, int BF, int OUT, int TA, int TB, bool FAST>
+//
+// Groups' tiles are counted on the device, from the offsets, so a workgroup first
+// reads those (one wave, 64 groups at a time) into a table in LDS and looks its tiles up there.
+// ROWS: every tile costs the same, so each XCD takes an eighth of them in a row
+// (one group's weights stay in one L2), a group's tiles in the order of map_tile.
+// COLUMNS: a group's tiles cost what its rows are, so each group's are dealt over all
+// XCDs, neighbours to one, and the next group's follow.  K is then the row stride of A and B;
+// the K loop runs over the group's blocks, of which there may be none.
+template <int AF, int BF, int OUT, int TA, int TB, bool FAST, Kind KIND = ONE>
 __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void gemm_block128_tile_kernel(
     int M, int N, int K, const uint8_t* __restrict__ A, ScaleRows sA, const uint8_t* __restrict__ B, ScaleRows sB,
-    void* __restrict__ D, int64_t ldd, Epilogue ep, int tiles_m, int tiles_n, int vec_ok) {
+    void* __restrict__ D, int64_t ldd, Epilogue ep, int tiles_m, int tiles_n, int vec_ok, GroupsArg grp) {
     using T = Tile<TA, TB>;
     constexpr bool WIDE = OUT == BSFP8_OUT_F32;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS_BYTES];
+    // (not there for ONE, which has no use of it)
+    __shared__ Tables tables;
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -128,31 +157,124 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
     const int wm = wave & 1;
     const int wn = wave >> 1;
     const int tiles = tiles_m * tiles_n;
-    const int real = (K + 127) >> 7;                 // stages that hold K values
-    const int nst = (real + 1) & ~1;                 // pairs, so that a stage's buffer is compile-time
-    const int ngr = (nst + 3) >> 2;
+
+    // A tile: its first row and column, the end of the rows that are its own, its
+    // group, the K blocks that hold values, and for COLUMNS the first block and scale word.
+    struct Place { int m0, n0, end, e, real, block, word; };
+    // its stages: pairs, so that a stage's buffer is compile-time
+    auto stages = [](const Place& p) { return KIND == COLUMNS && p.real == 0 ? 2 : (p.real + 1) & ~1; };
+    int share = 0, last = tiles;                     // ROWS: tiles per XCD; the tile numbers that count end here
+    if constexpr (KIND != ONE) {
+        if (wave == 0) {
+            const int limit = KIND == ROWS ? M : static_cast<int>(min(static_cast<int64_t>(K), int64_t(1) << 30));
+            groups::for_each<KIND == ROWS ? T::ROWS_A : 128>(grp.offsets, grp.count, limit, [&](const groups::Lane& g, bool in) {
+                if (in) {
+                    tables.at[g.e] = KIND == ROWS ? g.start : g.tile;
+                    tables.of[g.e] = KIND == ROWS ? g.tile : g.word;
+                    if (g.e == grp.count - 1) {
+                        tables.at[grp.count] = KIND == ROWS ? g.start + g.rows : g.tile + g.tiles;
+                        tables.of[grp.count] = KIND == ROWS ? g.tile + g.tiles : g.word + ((g.tiles + 3) >> 2);
+                    }
+                }
+                return false;
+            });
+        }
+        __syncthreads();
+        if constexpr (KIND == ROWS) {
+            const int total = __builtin_amdgcn_readfirstlane(tables.of[grp.count]) * tiles_n;
+            share = (total + 7) >> 3;
+            // this XCD's part of them, as the numbers x + 8 i of its tiles
+            last = 8 * max(0, min(share, total - static_cast<int>(blockIdx.x & 7) * share));
+        } else {
+            share = (tiles + 7) >> 3;
+            last = grp.count * 8 * share;
+        }
+    }
+    // The tile of number t < last, or (COLUMNS) the first that exists of t, t + step, ...: its number.
+    auto next_tile = [&](int t, int step) {
+        if constexpr (KIND == COLUMNS)
+            while (t < last && (t & 7) * share + ((t % (8 * share)) >> 3) >= tiles) t += step;
+        return t;
+    };
+    auto locate = [&](int t) {
+        Place p{};
+        int tm, tn;
+        p.real = (K + 127) >> 7;
+        p.end = M;
+        if constexpr (KIND == ONE) {
+            map_tile(t, tiles_m, tiles_n, 8, &tm, &tn);
+            p.m0 = tm * T::ROWS_A;
+        } else if constexpr (KIND == ROWS) {
+            t = (t & 7) * share + (t >> 3);
+            // the group whose tiles include row tile q of all: 16 groups, then one
+            const int q = t / tiles_n;
+            const uint64_t far = __ballot(tables.of[min(16 * (lane + 1), grp.count)] > q);
+            const int e0 = 16 * __builtin_ctzll(far);
+            const uint64_t near = __ballot(tables.of[min(e0 + (lane & 15) + 1, grp.count)] > q);
+            p.e = e0 + __builtin_ctzll(near);
+            const int first = __builtin_amdgcn_readfirstlane(tables.of[p.e]);
+            const int count = __builtin_amdgcn_readfirstlane(tables.of[p.e + 1]) - first;
+            t -= first * tiles_n;
+            const int g = t / (8 * tiles_n), rows = min(8, count - 8 * g), r = t - g * 8 * tiles_n;
+            tm = 8 * g + r % rows;
+            tn = r / rows;
+            p.m0 = __builtin_amdgcn_readfirstlane(tables.at[p.e]) + tm * T::ROWS_A;
+            p.end = __builtin_amdgcn_readfirstlane(tables.at[p.e + 1]);
+        } else {
+            p.e = t / (8 * share);
+            t = (t & 7) * share + ((t - p.e * 8 * share) >> 3);
+            const int g = t / (8 * tiles_n), rows = min(8, tiles_m - 8 * g), r = t - g * 8 * tiles_n;
+            tm = 8 * g + r % rows;
+            tn = r / rows;
+            p.m0 = tm * T::ROWS_A;
+            p.block = __builtin_amdgcn_readfirstlane(tables.at[p.e]);
+            p.word = __builtin_amdgcn_readfirstlane(tables.of[p.e]);
+            // what the buffers hold, whatever the offsets are
+            const int room = static_cast<int>(min(static_cast<int64_t>((K >> 7) - p.block), 4 * (grp.words - p.word)));
+            p.real = max(0, min(__builtin_amdgcn_readfirstlane(tables.at[p.e + 1]) - p.block, room));
+        }
+        p.n0 = tn * T::ROWS_B;
+        return p;
+    };
+    Place here;
+    int tile = next_tile(blockIdx.x, gridDim.x);
+    if (KIND != ONE && tile >= last) return;
+    here = locate(tile);
 
     // The loader: two stages ahead of the MFMAs, running on into the next tile.
     // The resources start at the tile's first row and end after its last row
     // inside the matrix: rows past the edge read as zero (all of them past the
     // last tile), offsets stay below 256 K < 2^31.
-    int l_tile = blockIdx.x, l_stage = 0;
+    int l_tile = tile, l_stage = 0, l_stages = stages(here), l_span = K;
     __amdgpu_buffer_rsrc_t rs_a, rs_b;
-    auto aim = [&]() {
-        int tm = 0, tn = 0;
-        const bool any = l_tile < tiles;
-        if (any) map_tile(l_tile, tiles_m, tiles_n, 8, &tm, &tn);
-        const int m0 = tm * T::ROWS_A, n0 = tn * T::ROWS_B;
-        rs_a = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(A) + static_cast<int64_t>(m0) * K, 0,
-                                                 any ? min(T::ROWS_A, M - m0) * K : 0, 0x00020000);
-        rs_b = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(B) + static_cast<int64_t>(n0) * K, 0,
-                                                 any ? min(T::ROWS_B, N - n0) * K : 0, 0x00020000);
+    auto aim = [&](const Place& p, bool any) {
+        const uint8_t* pa = A + static_cast<int64_t>(p.m0) * K;
+        const uint8_t* pb = B + static_cast<int64_t>(p.n0) * K;
+        int size_a = min(T::ROWS_A, p.end - p.m0) * K, size_b = min(T::ROWS_B, N - p.n0) * K;
+        if constexpr (KIND == ROWS) pb += static_cast<int64_t>(p.e) * N * K;
+        if constexpr (KIND == COLUMNS) {
+            // the group's part of the last row ends them
+            l_span = 128 * p.real;
+            pa += static_cast<int64_t>(p.block) * 128;
+            pb += static_cast<int64_t>(p.block) * 128;
+            size_a += l_span - K;
+            size_b += l_span - K;
+            any = any && l_span > 0;
+        }
+        rs_a = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(pa), 0, any ? size_a : 0, 0x00020000);
+        rs_b = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(pb), 0, any ? size_b : 0, 0x00020000);
     };
     auto advance = [&]() {
-        if (++l_stage == nst) {
+        if (++l_stage == l_stages) {
             l_stage = 0;
-            l_tile += gridDim.x;
-            aim();
+            l_tile = next_tile(l_tile + gridDim.x, gridDim.x);
+            const bool any = l_tile < last;
+            Place p{};
+            // (the lookup is the compiler's code: no fragment may still be on its way to a register)
+            if constexpr (KIND != ONE) lds_wait();
+            if (any) p = locate(l_tile);
+            if constexpr (KIND == COLUMNS) l_stages = stages(p);
+            aim(p, any);
         }
     };
     // Direct load j of wave w fills rows 8 g .. 8 g + 7 of A (j < 2 TA) or B,
@@ -170,22 +292,26 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
         constexpr int both = 4 * (TA < TB ? TA : TB);
         constexpr bool is_a = j < both ? (j & 1) == 0 : TA > TB;
         constexpr int gi = j < both ? j >> 1 : j - both / 2;
-        const uint32_t vo = l_stage * 128 + dchunk * 16 < K ? dma_row + gi * dma_grp : 0x80000000u;
+        const uint32_t vo = l_stage * 128 + dchunk * 16 < (KIND == COLUMNS ? l_span : K) ? dma_row + gi * dma_grp : 0x80000000u;
         lds_void* dst = (lds_void*)(lds + buf * T::STAGE_BYTES + (is_a ? 0 : T::A_BYTES) + (4 * gi + wave) * 1024);
         if constexpr (is_a)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, dst, 16, vo, l_stage * 128, 0, 0);
         else
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, dst, 16, vo, l_stage * 128, 0, 0);
     };
-    // Scale words of a group of the tile at (m0, n0): wave w brings rows
+    // Scale words of a group of K blocks of a tile: wave w brings rows
     // 16 TA w .. of A (q = 0), 16 TB w .. of B (q = 1); rows past the edge take
     // one that exists.
     int slot = 0;                                    // LDS slot of the group in use
-    auto scale_dma = [&](int m0, int n0, int group, int to, int q) {
+    auto scale_dma = [&](const Place& p, int group, int to, int q) {
         const int per = q == 0 ? 16 * TA : 16 * TB;
-        const int row = min((q == 0 ? m0 : n0) + per * wave + min(lane, per - 1), (q == 0 ? M : N) - 1);
+        const int row = min((q == 0 ? p.m0 : p.n0) + per * wave + min(lane, per - 1), (q == 0 ? p.end : N) - 1);
         const uint32_t* src = q == 0 ? sA.words + group * sA.rows + (row >> sA.shift)
                                      : sB.words + group * sB.rows + (row >> sB.shift);
+        if constexpr (KIND == ROWS) src += q == 0 ? 0 : static_cast<int64_t>(p.e) * ((((K + 127) >> 7) + 3) >> 2) * sB.rows;
+        // (a group without rows has no words; what is read in their place is not used)
+        if constexpr (KIND == COLUMNS)
+            src = p.real ? src + p.word * (q == 0 ? sA.rows : sB.rows) : reinterpret_cast<const uint32_t*>(grp.offsets);
         lds_void* dst = (lds_void*)(lds + T::SCALES + to * T::SCALE_GROUP + (q == 0 ? 0 : T::ROWS_A * 4) + wave * per * 4);
         if (lane < per) __builtin_amdgcn_global_load_lds(src, dst, 4, 0, 0);
     };
@@ -247,12 +373,12 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
         for (int t = 0; t < TA + TB; ++t) asm volatile("" : "+v"(v[t]));
     };
     // bytes past the last K block (their codes are zero) become a unit scale
-    const uint32_t used = (real & 3) ? (1u << (8 * (real & 3))) - 1u : 0xFFFFFFFFu;
-    auto take_scales = [&](int group) {
+    auto take_scales = [&](const Place& p, int group) {
+        const uint32_t used = (p.real & 3) ? (1u << (8 * (p.real & 3))) - 1u : KIND == COLUMNS && p.real == 0 ? 0u : 0xFFFFFFFFu;
         // named after the wait for their reads: the compiler takes them as
         // written when the read is issued
         name_scales(nxt);
-        const uint32_t keep = group == ngr - 1 ? used : 0xFFFFFFFFu;
+        const uint32_t keep = group == ((stages(p) + 3) >> 2) - 1 ? used : 0xFFFFFFFFu;
 #pragma unroll
         for (int t = 0; t < TA + TB; ++t) cur[t] = (nxt[t] & keep) | (0x7F7F7F7Fu & ~keep);
         // VALU writes settle before an MFMA of the assembly reads them
@@ -295,16 +421,12 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
         asm volatile("s_nop 1");
     };
 
-    int tile = blockIdx.x, tm, tn;
-    map_tile(tile, tiles_m, tiles_n, 8, &tm, &tn);
-    int m0 = tm * T::ROWS_A, n0 = tn * T::ROWS_B;
-
     // Prologue: stage 0, the first scale group and stage 1 on their way.
-    aim();
+    aim(here, true);
     static_for<T::NL>([&](auto J) { dma_one(J, C0); });
     advance();
-    scale_dma(m0, n0, 0, 0, 0);
-    scale_dma(m0, n0, 0, 0, 1);
+    scale_dma(here, 0, 0, 0);
+    scale_dma(here, 0, 0, 1);
     static_for<T::NL>([&](auto J) { dma_one(J, C1); });
     advance();
     asm volatile("s_waitcnt vmcnt(%0)" :: "i"(T::NL) : "memory");
@@ -316,27 +438,24 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
         static_for<TA + TB>([&](auto R) { read_half(R, hs[0], C0, C0); });
         static_for<TA + TB>([&](auto R) { read_half(R, hs[1], C0, C1); });
         lds_wait();
-        take_scales(0);
+        take_scales(here, 0);
         take_floats(0);
         static_for<4 * (TA + TB)>([&](auto P) { widen_one(P, C0); });
     }
 
     bool stores = false;                             // an epilogue's stores may be in flight
     for (;;) {
-        int nm0 = m0, nn0 = n0;
-        const bool more = tile + static_cast<int>(gridDim.x) < tiles;
-        if (more) {
-            map_tile(tile + gridDim.x, tiles_m, tiles_n, 8, &tm, &tn);
-            nm0 = tm * T::ROWS_A;
-            nn0 = tn * T::ROWS_B;
-        }
+        Place there = here;
+        const int next = next_tile(tile + gridDim.x, gridDim.x), nst = stages(here), ngr = (nst + 3) >> 2;
+        const bool more = next < last;
+        if (more) there = locate(next);
         auto run_stage = [&](int s, auto U) {
             constexpr int u = U;                     // stage within its scale group
             constexpr auto cb = std::integral_constant<int, u & 1>{};
             constexpr auto nb = std::integral_constant<int, (u & 1) ^ 1>{};
             lds_wait();
             if constexpr (u == 0) {
-                take_scales(s >> 2);
+                take_scales(here, s >> 2);
             }
             const bool group_end = u == 3 || (u == 1 && s + 1 == nst);
             static_for<2 * T::NM>([&](auto N_) {
@@ -377,8 +496,8 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
                 // group's first stage, read in its last
                 if constexpr (u == 0 && n == T::READY + 1) {
                     const bool in = (s >> 2) + 1 < ngr;
-                    scale_dma(in ? m0 : nm0, in ? n0 : nn0, in ? (s >> 2) + 1 : 0, slot ^ 1, 0);
-                    scale_dma(in ? m0 : nm0, in ? n0 : nn0, in ? (s >> 2) + 1 : 0, slot ^ 1, 1);
+                    scale_dma(in ? here : there, in ? (s >> 2) + 1 : 0, slot ^ 1, 0);
+                    scale_dma(in ? here : there, in ? (s >> 2) + 1 : 0, slot ^ 1, 1);
                 }
                 if constexpr ((u & 1) && n == 2 * T::NM - 2) {
                     if (group_end) {
@@ -410,8 +529,8 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
                     if constexpr (cb == 0) {
                         if (u == 0) {
                             const bool in = (s >> 2) + 1 < ngr;
-                            scale_dma(in ? m0 : nm0, in ? n0 : nn0, in ? (s >> 2) + 1 : 0, slot ^ 1, 0);
-                            scale_dma(in ? m0 : nm0, in ? n0 : nn0, in ? (s >> 2) + 1 : 0, slot ^ 1, 1);
+                            scale_dma(in ? here : there, in ? (s >> 2) + 1 : 0, slot ^ 1, 0);
+                            scale_dma(in ? here : there, in ? (s >> 2) + 1 : 0, slot ^ 1, 1);
                         }
                     } else if (group_end) {
                         slot ^= 1;
@@ -420,7 +539,7 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
                 }
                 if constexpr (q == 7) {
                     if constexpr (cb == 1) {
-                        if (group_end) take_scales(s + 1 == nst ? 0 : (s + 1) >> 2);
+                        if (group_end) take_scales(s + 1 == nst ? there : here, s + 1 == nst ? 0 : (s + 1) >> 2);
                     }
                     take_floats(group_end ? 0 : u + 1);
                 }
@@ -486,18 +605,80 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
         // (The lane is opaque here, so that the epilogue's addresses are not kept
         // in registers through the main loop.)
         uint8_t* strip = lds + T::STRIPS + wave * kStripBytes;
-        const int mw = m0 + wm * 32 * TA, nw = n0 + wn * 32 * TB;
+        const int mw = here.m0 + wm * 32 * TA, nw = here.n0 + wn * 32 * TB;
+        void* out = D;
+        Epilogue fin = ep;
+        if constexpr (KIND == COLUMNS) {
+            constexpr int es = OUT == BSFP8_OUT_F32 ? 4 : 2;
+            out = static_cast<uint8_t*>(D) + here.e * grp.d_group * es;
+            if (ep.c) fin.c = static_cast<const uint8_t*>(ep.c) + here.e * grp.c_group * es;
+        }
         int el = lane;
         asm volatile("" : "+v"(el));
         const int srow = el >> 3, schunk = el & 7;
         uint8_t* put = strip + (el & 31) * 128;
         const int psw = (el >> 1) & 7, phalf = el >> 5;
-        if constexpr (FAST) {
-            static_assert(OUT == BSFP8_OUT_BF16 && TB % 2 == 0, "bf16 output, column pairs");
+        if constexpr (FAST && WIDE) {
+            // strips of 32 rows x 32 columns; C, if any, kAhead strips ahead of its use (one
+            // ahead, a CU has 16 KB of it in flight, where HBM needs some 40)
+            constexpr int es = 4, STRIPS = TA * TB, kAhead = STRIPS < 4 ? STRIPS : 4;
+            const __amdgpu_buffer_rsrc_t rs_d = __builtin_amdgcn_make_buffer_rsrc(
+                static_cast<uint8_t*>(out) + static_cast<int64_t>(here.m0) * ldd * es, 0,
+                min(T::ROWS_A, here.end - here.m0) * static_cast<int>(ldd) * es, 0x00020000);
+            const __amdgpu_buffer_rsrc_t rs_c = __builtin_amdgcn_make_buffer_rsrc(
+                static_cast<uint8_t*>(const_cast<void*>(fin.c)) + static_cast<int64_t>(here.m0) * fin.ldc * es, 0,
+                min(T::ROWS_A, here.end - here.m0) * static_cast<int>(fin.ldc) * es, 0x00020000);
+            const uint32_t ld4 = static_cast<uint32_t>(ldd) * es, lc4 = static_cast<uint32_t>(fin.ldc) * es;
+            const int row = wm * 32 * TA + srow;
+            auto column = [&](int ti) { return nw + 32 * ti + 4 * schunk; };
+            u32x4 c[kAhead][4];
+            auto fetch_c = [&](auto S) {
+                constexpr int tj = S / TB, ti = S % TB;
+                const uint32_t at = column(ti) < N ? row * lc4 + column(ti) * es : 0x80000000u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const auto w = __builtin_amdgcn_raw_buffer_load_b128(rs_c, at + (32 * tj + 8 * i) * lc4, 0, 0);
+                    c[S % kAhead][i] = u32x4{w[0], w[1], w[2], w[3]};
+                }
+            };
+            if (fin.beta != 0.0f) static_for<kAhead>([&](auto S) { fetch_c(S); });
+            static_for<STRIPS>([&](auto S) {
+                constexpr int tj = S / TB, ti = S % TB;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const v16f& a = acc[ti][tj];
+                    *reinterpret_cast<float4*>(put + (((2 * q + phalf) ^ psw) << 4)) =
+                        make_float4(a[4 * q + 0], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
+                }
+                __builtin_amdgcn_wave_barrier();
+                const uint32_t at = column(ti) < N ? row * ld4 + column(ti) * es : 0x80000000u;
+                u32x4 w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int R = 8 * i + srow;
+                    const float4 v = *reinterpret_cast<const float4*>(strip + R * 128 + ((schunk ^ ((R >> 1) & 7)) << 4));
+                    w[i] = u32x4{__float_as_uint(fin.alpha * v.x), __float_as_uint(fin.alpha * v.y),
+                                 __float_as_uint(fin.alpha * v.z), __float_as_uint(fin.alpha * v.w)};
+                }
+                if (fin.beta != 0.0f) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            w[i][j] = __float_as_uint(fmaf(fin.beta, __uint_as_float(c[S % kAhead][i][j]), __uint_as_float(w[i][j])));
+                    if constexpr (S + kAhead < STRIPS) fetch_c(std::integral_constant<int, S + kAhead>{});
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    __builtin_amdgcn_raw_buffer_store_b128(w[i], rs_d, at + (32 * tj + 8 * i) * ld4, 0, 0);
+                __builtin_amdgcn_wave_barrier();
+            });
+        } else if constexpr (FAST) {
+            static_assert(OUT != BSFP8_OUT_F32 && TB % 2 == 0, "16-bit output, column pairs");
             // strips of 32 rows x 64 columns of 16-bit outputs
             const __amdgpu_buffer_rsrc_t rs_d = __builtin_amdgcn_make_buffer_rsrc(
-                static_cast<uint16_t*>(D) + static_cast<int64_t>(m0) * ldd, 0,
-                min(T::ROWS_A, M - m0) * static_cast<int>(ldd) * 2, 0x00020000);
+                static_cast<uint16_t*>(out) + static_cast<int64_t>(here.m0) * ldd, 0,
+                min(T::ROWS_A, here.end - here.m0) * static_cast<int>(ldd) * 2, 0x00020000);
             // byte offset of this lane's first chunk of each column pair; past
             // column N one that stays out of range whatever rows are added
             const uint32_t ld2 = static_cast<uint32_t>(ldd) * 2;
@@ -516,8 +697,13 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const v16f& a = acc[2 * tp + t][tj];
-                            *reinterpret_cast<uint2*>(put + (((4 * t + q) ^ psw) << 4) + 8 * phalf) =
-                                make_uint2(bf16_pair(a[4 * q + 0], a[4 * q + 1]), bf16_pair(a[4 * q + 2], a[4 * q + 3]));
+                            uint2 w;
+                            if constexpr (KIND == ONE)
+                                w = make_uint2(bf16_pair(a[4 * q + 0], a[4 * q + 1]), bf16_pair(a[4 * q + 2], a[4 * q + 3]));
+                            else
+                                w = make_uint2(half_pair<OUT>(ep.alpha * a[4 * q + 0], ep.alpha * a[4 * q + 1]),
+                                               half_pair<OUT>(ep.alpha * a[4 * q + 2], ep.alpha * a[4 * q + 3]));
+                            *reinterpret_cast<uint2*>(put + (((4 * t + q) ^ psw) << 4) + 8 * phalf) = w;
                         }
                     __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -543,12 +729,22 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
                             make_float4(a[4 * q + 0], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
                     }
                     __builtin_amdgcn_wave_barrier();
+                    if constexpr (KIND == ONE) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int R = 8 * i + srow;
-                        const float4 v = *reinterpret_cast<const float4*>(strip + R * 128 + ((schunk ^ ((R >> 1) & 7)) << 4));
-                        const float a4[4] = {v.x, v.y, v.z, v.w};
-                        finish_row_chunk<OUT, 4>(D, ldd, ep, mw + 32 * tj + R, nw + 32 * ti + 4 * schunk, M, N, vec_ok, a4);
+                        for (int i = 0; i < 4; ++i) {
+                            const int R = 8 * i + srow;
+                            const float4 v = *reinterpret_cast<const float4*>(strip + R * 128 + ((schunk ^ ((R >> 1) & 7)) << 4));
+                            const float a4[4] = {v.x, v.y, v.z, v.w};
+                            finish_row_chunk<OUT, 4>(out, ldd, fin, mw + 32 * tj + R, nw + 32 * ti + 4 * schunk, here.end, N, vec_ok, a4);
+                        }
+                    } else {
+                        // (not unrolled: with every strip's edges written out, this tile took minutes to compile)
+#pragma unroll 1
+                        for (int i = 0; i < 4; ++i) {
+                            const int R = 8 * i + srow;
+                            const float4 v = *reinterpret_cast<const float4*>(strip + R * 128 + ((schunk ^ ((R >> 1) & 7)) << 4));
+                            finish_chunk<OUT>(out, ldd, fin, mw + 32 * tj + R, nw + 32 * ti + 4 * schunk, here.end, N, v);
+                        }
                     }
                     __builtin_amdgcn_wave_barrier();
                 }
@@ -557,9 +753,8 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
         }
         if (!T::PERSISTENT || !more) break;
         clear();
-        tile += gridDim.x;
-        m0 = nm0;
-        n0 = nn0;
+        tile = next;
+        here = there;
     }
     // no direct load may still be writing LDS when the workgroup ends, and the
     // last reads, which have no consumer, are named after the wait so that
@@ -589,7 +784,7 @@ hipError_t launch_typed(const TileArgs& t) {
     hipLaunchKernelGGL((gemm_block128_tile_kernel<AF, BF, OUT, TA, TB, FAST>), dim3(static_cast<uint32_t>(grid)),
                        dim3(kThreads), 0, t.stream, static_cast<int>(t.M), static_cast<int>(t.N),
                        static_cast<int>(t.K), t.a, t.sa, t.b, t.sb, t.d, t.ldd, t.ep, static_cast<int>(tm),
-                       static_cast<int>(tn), vec16_ok(OUT, t.d, t.ldd, t.ep));
+                       static_cast<int>(tn), vec16_ok(OUT, t.d, t.ldd, t.ep), GroupsArg{});
     return hipGetLastError();
 }
 
@@ -615,6 +810,45 @@ hipError_t launch_tile(const TileArgs& t) {
                                      : launch_out<BSFP8_E4M3, BSFP8_E5M2, TA, TB, F32>(t);
     return t.b_fmt == BSFP8_E4M3 ? launch_out<BSFP8_E5M2, BSFP8_E4M3, TA, TB, F32>(t)
                                  : launch_out<BSFP8_E5M2, BSFP8_E5M2, TA, TB, F32>(t);
+}
+
+// The same for products grouped by rows and by columns.  Workgroups: one per CU, or (the smallest tile)
+// one per tile, as many as there can be; a multiple of 8, so that a workgroup's tiles stay on its XCD.
+inline int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
+
+template <int AF, int BF, int OUT, int TA, int TB, bool FAST>
+hipError_t launch_rows(const GroupedArgs& t) {
+    const int64_t tn = (t.N + 64 * TB - 1) / (64 * TB), tiles = (t.M / (64 * TA) + (t.M < t.groups ? t.M : t.groups)) * tn;
+    const int64_t grid = Tile<TA, TB>::PERSISTENT && tiles > kPersistent ? kPersistent : up8(tiles);
+    hipLaunchKernelGGL((gemm_block128_tile_kernel<AF, BF, OUT, TA, TB, FAST, ROWS>), dim3(static_cast<uint32_t>(grid)),
+                       dim3(kThreads), 0, t.stream, static_cast<int>(t.M), static_cast<int>(t.N),
+                       static_cast<int>(t.K), t.a, t.sa, t.b, t.sb, t.d, t.ldd, t.ep, 0, static_cast<int>(tn),
+                       0, GroupsArg{t.offsets, t.groups, 0, 0, 0});
+    return hipGetLastError();
+}
+
+template <int AF, int BF, int OUT, int TA, int TB, bool FAST>
+hipError_t launch_columns(const GroupedKArgs& t) {
+    const int64_t tm = (t.M + 64 * TA - 1) / (64 * TA), tn = (t.N + 64 * TB - 1) / (64 * TB);
+    const int64_t tiles = up8(tm * tn) * t.groups;
+    const int64_t grid = Tile<TA, TB>::PERSISTENT && tiles > kPersistent ? kPersistent : tiles;
+    const ScaleRows sa{t.sa, t.M, 0}, sb{t.sb, t.N, 0};
+    hipLaunchKernelGGL((gemm_block128_tile_kernel<AF, BF, OUT, TA, TB, FAST, COLUMNS>), dim3(static_cast<uint32_t>(grid)),
+                       dim3(kThreads), 0, t.stream, static_cast<int>(t.M), static_cast<int>(t.N),
+                       static_cast<int>(t.columns), t.a, sa, t.b, sb, t.d, t.ldd, t.ep, static_cast<int>(tm),
+                       static_cast<int>(tn), 0, GroupsArg{t.offsets, t.groups, t.words, t.d_group, t.c_group});
+    return hipGetLastError();
+}
+
+// FAST where the call allows it (fast_ok), else the general form, where the tile has one (GENERAL).
+template <int TA, int TB, bool GENERAL>
+hipError_t launch_grouped_tile(const GroupedArgs& t) {
+    return by_type(t, [](auto AF, auto BF, auto OUT, const GroupedArgs& g) {
+        if constexpr (!GENERAL && OUT == BSFP8_OUT_F32) return hipErrorInvalidValue;
+        else if (g.fast_ok()) return launch_rows<AF, BF, OUT, TA, TB, true>(g);
+        else if constexpr (GENERAL) return launch_rows<AF, BF, OUT, TA, TB, false>(g);
+        else return hipErrorInvalidValue;
+    });
 }
 
 }  // namespace

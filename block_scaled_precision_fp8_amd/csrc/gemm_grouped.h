@@ -6,6 +6,14 @@
 
 namespace bsfp8 {
 
+// What the tiled forms' constant-count epilogue takes: whole 16-byte chunks of D (and C), 32-bit
+// offsets within a tile's rows, and C for FP32 output only.
+inline bool fast_epilogue(int out, int64_t N, const void* d, int64_t ldd, const Epilogue& ep) {
+    constexpr int64_t most = int64_t(1) << 21;
+    return vec16_ok(out, d, ldd, ep) && N % (out == BSFP8_OUT_F32 ? 4 : 8) == 0 && ldd < most && ep.ldc < most &&
+           (out == BSFP8_OUT_F32 || ep.beta == 0.0f);
+}
+
 // D[i] = alpha A[i] B[e(i)]^T (+ beta C[i]): b and its scales are `groups`
 // matrices one after another; sb.words points to the first one's.
 struct GroupedArgs {
@@ -23,8 +31,13 @@ struct GroupedArgs {
     int64_t ldd;
     Epilogue ep;
     hipStream_t stream;
+    bool fast_ok() const { return fast_epilogue(out, N, d, ldd, ep); }
 };
 hipError_t launch_gemm_grouped(const GroupedArgs& t);
+hipError_t launch_gemm_grouped_rows(const GroupedArgs& t);
+hipError_t launch_gemm_grouped_4x4(const GroupedArgs& t);
+hipError_t launch_gemm_grouped_2x2(const GroupedArgs& t);
+hipError_t launch_gemm_grouped_1x2(const GroupedArgs& t);
 
 // D[e] = alpha sum over group e's columns i of A[:, i] B[:, i]^T (+ beta C[e]):
 // K values `columns` to a row, each group's from a multiple of 128 on and its scales from a word on.
@@ -43,9 +56,81 @@ struct GroupedKArgs {
     int64_t ldd, d_group, c_group;
     Epilogue ep;
     hipStream_t stream;
+    bool fast_ok() const {
+        const int64_t es = out == BSFP8_OUT_F32 ? 4 : 2;
+        return fast_epilogue(out, N, d, ldd, ep) &&
+               (groups == 1 || ((d_group * es) % 16 == 0 && (ep.beta == 0.0f || (c_group * es) % 16 == 0)));
+    }
 };
-
 hipError_t launch_gemm_grouped_wgrad(const GroupedKArgs& t);
+hipError_t launch_gemm_wgrad_narrow(const GroupedKArgs& t);
+hipError_t launch_gemm_wgrad_4x4(const GroupedKArgs& t);           // 16-bit outputs
+hipError_t launch_gemm_wgrad_4x4_f32(const GroupedKArgs& t);
+hipError_t launch_gemm_wgrad_2x2(const GroupedKArgs& t);
+
+// finish_row_chunk for four columns at any alignment: a whole chunk moves in one access (the hardware
+// takes any element's address).  With D of 2001 columns 32 products 1000 x 2001 x 69 took
+// 106 us element by element, 81 so.
+template <int OUT>
+__device__ __forceinline__ void finish_chunk(void* D, int64_t ldd, const Epilogue& ep, int m, int n, int M, int N, float4 acc) {
+    typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
+    typedef uint32_t h4 __attribute__((ext_vector_type(2), aligned(2)));
+    if (m >= M || n >= N) return;
+    const bool whole = n + 4 <= N;
+    float v[4] = {ep.alpha * acc.x, ep.alpha * acc.y, ep.alpha * acc.z, ep.alpha * acc.w};
+    if (ep.beta != 0.0f) {
+        const int64_t at = static_cast<int64_t>(m) * ep.ldc + n;
+        float c[4] = {};
+        if constexpr (OUT == BSFP8_OUT_F32) {
+            const float* p = static_cast<const float*>(ep.c) + at;
+            if (whole) {
+                const f4 w = *reinterpret_cast<const f4*>(p);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) c[j] = w[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+                    if (n + j < N) c[j] = p[j];
+            }
+        } else {
+            const uint16_t* p = static_cast<const uint16_t*>(ep.c) + at;
+            if (whole) {
+                const h4 w = *reinterpret_cast<const h4*>(p);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) c[j] = from_half_bits<OUT>(static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1))));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+                    if (n + j < N) c[j] = from_half_bits<OUT>(p[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = fmaf(ep.beta, c[j], v[j]);
+    }
+    const int64_t at = static_cast<int64_t>(m) * ldd + n;
+    if constexpr (OUT == BSFP8_OUT_F32) {
+        float* p = static_cast<float*>(D) + at;
+        if (whole) {
+            *reinterpret_cast<f4*>(p) = f4{v[0], v[1], v[2], v[3]};
+        } else {
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                if (n + j < N) p[j] = v[j];
+        }
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(D) + at;
+        uint16_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = to_half_bits<OUT>(v[j]);
+        if (whole) {
+            *reinterpret_cast<h4*>(p) = h4{h[0] | (static_cast<uint32_t>(h[1]) << 16), h[2] | (static_cast<uint32_t>(h[3]) << 16)};
+        } else {
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                if (n + j < N) p[j] = h[j];
+        }
+    }
+}
 
 // launch(A's format, B's format, output type, args) with the three as constants.
 template <class T, class F>

@@ -1,0 +1,88 @@
+// gemm_grouped.hip -- which form a grouped block-of-128 FP8 product runs on (gfx950).
+//
+// The groups' sizes are on the device, so the choice goes by their number and the rows in all: as if
+// the rows were spread evenly, half a tile of each group empty.  Times are microseconds on MI355X.
+#include "gemm_grouped.h"
+
+#include <algorithm>
+
+namespace bsfp8 {
+
+namespace {
+
+enum Form { FEW, T64x128, T128, T256 };
+
+// Rows by expert.  A tiled form runs `stage` per 128 K and tile on each CU, and `tile` besides; the
+// form for few rows moves 32 bytes per K and 16 x 16 tile at 10 TB/s; every form reads the
+// weights of the groups that have rows at 5 TB/s, which hides behind the products by some 70%.
+// 64 groups, N 2048, K 4096, 16-bit output (few rows, 64 x 128, 128 x 128, 256 x 256): 128 rows 73, 97, 101,
+// 108; 512 rows 118, 120, 123, 126; 1024 rows 172, 122, 127, 130; 4096 rows 545, 130, 147, 167; 8192
+// rows 1019, 160, 150, 174; 16384 rows 2005, 238, 204, 176.  16384 rows of 8 groups, N 14336: -,
+// 1334, 1037, 770; 8 rows of 16 groups, N 1024: 8.6, 15.9, 17.2, 37.4.
+Form choose_rows(const GroupedArgs& t) {
+    const bool wide = t.out == BSFP8_OUT_F32;
+    const double M = static_cast<double>(t.M), N = static_cast<double>(t.N), K = static_cast<double>(t.K);
+    const double groups = static_cast<double>(std::min<int64_t>(t.M, t.groups)), stages = std::max(1.0, K / 128.0);
+    const double weights = groups * N * K / 5.0e6;
+    auto row_tiles = [&](double rows) { return std::max(groups, M / rows + groups / 2); };
+    auto total = [&](double products) { return 4.0 + std::max(weights, products) + 0.3 * std::min(weights, products); };
+    Form form = FEW;
+    // (a workgroup of up to 1024 threads per 16 columns and group; threads are counted in 32 bits)
+    double best = 4.0 + std::max(groups * N * K / 6.0e6, row_tiles(16) * (N / 16.0) * K * 32.0 / 10.0e6);
+    if ((t.N + 15) / 16 * t.groups >= int64_t(1) << 22) best = 1e300;
+    struct Cost { Form form; int rows, columns; double stage, stage_f32, tile; };
+    static constexpr Cost kCost[3] = {{T64x128, 64, 128, 0.37, 0.51, 0.0}, {T128, 128, 128, 0.56, 0.88, 0.0}, {T256, 256, 256, 1.35, 1e9, 8.0}};
+    for (const Cost& c : kCost) {
+        if (c.form == T256 && (wide || !t.fast_ok())) continue;
+        const double tiles = row_tiles(c.rows) * std::max(1.0, N / c.columns) / 256.0;
+        const double rounds = c.form == T256 ? static_cast<double>(static_cast<int64_t>(tiles + 1.0)) : std::max(1.0, tiles);
+        const double time = total(rounds * (stages * (wide ? c.stage_f32 : c.stage) + c.tile));
+        if (time < best) {
+            best = time;
+            form = c.form;
+        }
+    }
+    return form;
+}
+
+// K values by expert.  Narrow: 32 x 32 tiles, three workgroups per CU, K over four waves.
+// 8192 rows of 4 groups, 256 x 256 (narrow, 128 x 128, 256 x 256): 8.6, 17, 35; 300 rows of 8 groups, 256 x 256:
+// 5.3, 7.2, 15; 64 rows of 64 groups, 512 x 512: 81, 17, 22; 2222 rows of 32 groups, 1000 x 2000: 327,
+// 68, 61; 16384 rows of 8 groups, 4096 x 4096: -, 353, 256, and FP32 -, 523, 444.
+Form choose_columns(const GroupedKArgs& t) {
+    const bool wide = t.out == BSFP8_OUT_F32;
+    // (columns: the rows in all and up to 127 more per group)
+    const double blocks = std::max(1.0, static_cast<double>(t.columns) / 128.0 / t.groups);
+    auto tiles = [&](int64_t side) { return static_cast<double>((t.M + side - 1) / side * ((t.N + side - 1) / side) * t.groups); };
+    const double few = tiles(32);
+    double best = 4.0 + (few <= 768 ? 0.22 * blocks + 1.5 : few / 768 * (0.22 * blocks + 3.7));
+    if (few >= (1 << 24)) best = 1e300;              // threads are counted in 32 bits
+    Form form = FEW;
+    const double t128 = 4.0 + std::max(1.0, tiles(128) / 256) * (blocks * (wide ? 0.88 : 0.56) + 2.5);
+    if (t128 < best) best = t128, form = T128;
+    const double t256 = 4.0 + static_cast<double>(static_cast<int64_t>((tiles(256) + 255) / 256)) * (blocks * (wide ? 3.05 : 1.35) + 9.0);
+    if (t.fast_ok() && t256 < best) form = T256;
+    return form;
+}
+
+}  // namespace
+
+hipError_t launch_gemm_grouped(const GroupedArgs& t) {
+    if (t.K == 0) return launch_gemm_grouped_rows(t);
+    switch (choose_rows(t)) {
+    case T64x128: return launch_gemm_grouped_1x2(t);
+    case T128: return launch_gemm_grouped_2x2(t);
+    case T256: return launch_gemm_grouped_4x4(t);
+    default: return launch_gemm_grouped_rows(t);
+    }
+}
+
+hipError_t launch_gemm_grouped_wgrad(const GroupedKArgs& t) {
+    switch (choose_columns(t)) {
+    case T128: return launch_gemm_wgrad_2x2(t);
+    case T256: return t.out == BSFP8_OUT_F32 ? launch_gemm_wgrad_4x4_f32(t) : launch_gemm_wgrad_4x4(t);
+    default: return launch_gemm_wgrad_narrow(t);
+    }
+}
+
+}  // namespace bsfp8

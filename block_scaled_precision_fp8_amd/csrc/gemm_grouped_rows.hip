@@ -21,7 +21,7 @@ constexpr int kMaxWaves = 16;
 template <int AF, int BF, int OUT>
 __global__ __launch_bounds__(64 * kMaxWaves) void gemm_grouped_rows_kernel(
     int M, int N, int K, const int32_t* __restrict__ offsets, const uint8_t* __restrict__ A, ScaleRows sA,
-    const uint8_t* __restrict__ B, ScaleRows sB, void* __restrict__ D, int64_t ldd, Epilogue ep, int vec_ok, int tiles_n) {
+    const uint8_t* __restrict__ B, ScaleRows sB, void* __restrict__ D, int64_t ldd, Epilogue ep, int tiles_n) {
     __shared__ v4f part[kMaxWaves][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -70,8 +70,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemm_grouped_rows_kernel(
         if (wave == 0) {
             for (int w = 1; w < waves; ++w) acc += part[w][lane];
             // lane (r, q) holds row r, columns n0 + 4 q ..
-            const float a4[4] = {acc[0], acc[1], acc[2], acc[3]};
-            finish_row_chunk<OUT, 4>(D, ldd, ep, m0 + r, n0 + 4 * q, end, N, vec_ok, a4);
+            finish_chunk<OUT>(D, ldd, ep, m0 + r, n0 + 4 * q, end, N, make_float4(acc[0], acc[1], acc[2], acc[3]));
         }
         __syncthreads();
     }
@@ -85,13 +84,13 @@ hipError_t launch_out(const GroupedArgs& t) {
     hipLaunchKernelGGL((gemm_grouped_rows_kernel<AF, BF, OUT>), dim3(static_cast<uint32_t>(tn * t.groups)),
                        dim3(64 * waves), 0, t.stream, static_cast<int>(t.M), static_cast<int>(t.N),
                        static_cast<int>(t.K), t.offsets, t.a, t.sa, t.b, t.sb, t.d, t.ldd, t.ep,
-                       vec16_ok(OUT, t.d, t.ldd, t.ep), static_cast<int>(tn));
+                       static_cast<int>(tn));
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_gemm_grouped(const GroupedArgs& t) {
+hipError_t launch_gemm_grouped_rows(const GroupedArgs& t) {
     return by_type(t, [](auto AF, auto BF, auto OUT, const GroupedArgs& g) { return launch_out<AF, BF, OUT>(g); });
 }
 

@@ -25,7 +25,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void gemm_grouped_wgrad_kernel(
     int M, int N, int64_t columns, int64_t words, int count, const int32_t* __restrict__ offsets,
     const uint8_t* __restrict__ A, const uint32_t* __restrict__ sA, const uint8_t* __restrict__ B,
     const uint32_t* __restrict__ sB, void* __restrict__ D, int64_t ldd, int64_t d_group, int64_t c_group, Epilogue ep,
-    int tiles_m, int tiles_n, int vec_ok) {
+    int tiles_m, int tiles_n) {
     __shared__ v16f part[kWaves - 1][64];
     __shared__ __attribute__((aligned(16))) uint8_t stage[kWaves][2][32 * 128];
     const int lane = threadIdx.x & 63;
@@ -113,27 +113,24 @@ __global__ __launch_bounds__(64 * kWaves, 2) void gemm_grouped_wgrad_kernel(
     // lane (r, h) holds row m0 + r, columns n0 + 8 q + 4 h + i in acc[4 q + i]
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const float a4[4] = {acc[4 * q + 0], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
-        finish_row_chunk<OUT, 4>(d, ldd, ep, m0 + r, n0 + 8 * q + 4 * h, M, N, vec_ok, a4);
+        finish_chunk<OUT>(d, ldd, ep, m0 + r, n0 + 8 * q + 4 * h, M, N,
+                          make_float4(acc[4 * q + 0], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]));
     }
 }
 
 template <int AF, int BF, int OUT>
 hipError_t launch_out(const GroupedKArgs& t) {
-    const int64_t es = OUT == BSFP8_OUT_F32 ? 4 : 2;
     const int tm = static_cast<int>((t.M + 31) / 32), tn = static_cast<int>((t.N + 31) / 32);
-    const bool whole = (t.d_group * es) % 16 == 0 && (t.ep.beta == 0.0f || (t.c_group * es) % 16 == 0);
     hipLaunchKernelGGL((gemm_grouped_wgrad_kernel<AF, BF, OUT>),
                        dim3(static_cast<uint32_t>(static_cast<int64_t>(tm) * tn * t.groups)), dim3(64 * kWaves), 0,
                        t.stream, static_cast<int>(t.M), static_cast<int>(t.N), t.columns, t.words, t.groups, t.offsets,
-                       t.a, t.sa, t.b, t.sb, t.d, t.ldd, t.d_group, t.c_group, t.ep, tm, tn,
-                       whole ? vec16_ok(OUT, t.d, t.ldd, t.ep) : 0);
+                       t.a, t.sa, t.b, t.sb, t.d, t.ldd, t.d_group, t.c_group, t.ep, tm, tn);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_gemm_grouped_wgrad(const GroupedKArgs& t) {
+hipError_t launch_gemm_wgrad_narrow(const GroupedKArgs& t) {
     return by_type(t, [](auto AF, auto BF, auto OUT, const GroupedKArgs& g) { return launch_out<AF, BF, OUT>(g); });
 }
 

@@ -527,7 +527,9 @@ bsfp8_status fp8_quantize_grouped_block128(const void* x, bsfp8_out x_type, int6
  * a: M x K codes, a_scales E8M0 words [ceil(K / 512)][M][4] (1 x 128 blocks); b: `groups`
  * matrices of N x K codes, one after another, b_scales likewise [groups][ceil(K / 512)][R][4], R = N or
  * ceil(N / 128) for b_block_rows 1 or 128.  alpha, c, ldc, beta, out, d, ldd, the
- * limits on N and K and the accuracy: as for scaled_gemm_block128.
+ * limits on N and K and the accuracy: as for scaled_gemm_block128.  At most 2^24 - 16 tiles of
+ * 64 x 128 ((M / 64 + groups) ceil(N / 128)).  The kernel form is chosen by the sizes, the
+ * number of groups and the output alone: equal calls give equal bits.
  */
 bsfp8_status scaled_gemm_grouped_block128(int64_t M, int64_t N, int64_t K, int64_t groups, const int32_t* offsets,
                                           bsfp8_format a_fmt, const void* a, const void* a_scales, bsfp8_format b_fmt,
@@ -543,7 +545,8 @@ bsfp8_status scaled_gemm_grouped_block128(int64_t M, int64_t N, int64_t K, int64
  * transposes that fp8_quantize_grouped_block128 wrote with the same offsets.  columns below 2^23
  * (BSFP8_ERR_UNSUPPORTED).  d: `groups` matrices of M x N, d_group elements apart (at least
  * (M - 1) ldd + N with more than one group), c likewise (c_group).  A group without
- * rows gives beta C (zeros for beta == 0).  Otherwise as scaled_gemm_block128.
+ * rows gives beta C (zeros for beta == 0).  At most 2^23 tiles of 128 x 128 in all, each
+ * group's padded to 8.  Otherwise as scaled_gemm_block128.
  */
 bsfp8_status scaled_gemm_grouped_wgrad_block128(int64_t M, int64_t N, int64_t columns, int64_t words, int64_t groups,
                                                 const int32_t* offsets, bsfp8_format a_fmt, const void* a,
