@@ -23,22 +23,26 @@ struct Lane {
     int word;                    // the first of its words of four tiles
 };
 
-// Inclusive scans over a wave.
-__device__ __forceinline__ int scan_add(int v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int u = __shfl_up(v, d);
-        v += lane >= d ? u : 0;
-    }
-    return v;
+// Inclusive scans over a wave, of values >= 0: within 16 lanes, then across them, by lane moves on the
+// VALU (through LDS shuffles three scans take about a microsecond, which every workgroup waits for).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int moved(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
 }
-__device__ __forceinline__ int scan_max(int v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int u = __shfl_up(v, d);
-        v = lane >= d ? max(v, u) : v;
-    }
-    return v;
+template <class F>
+__device__ __forceinline__ int scan(int v, F&& f) {
+    v = f(v, moved<0x111, 0xF>(v));              // row_shr 1, 2, 4, 8
+    v = f(v, moved<0x112, 0xF>(v));
+    v = f(v, moved<0x114, 0xF>(v));
+    v = f(v, moved<0x118, 0xF>(v));
+    v = f(v, moved<0x142, 0xA>(v));              // lane 15 of a row to the next one
+    return f(v, moved<0x143, 0xC>(v));           // lane 31 to the upper half
+}
+__device__ __forceinline__ int scan_add(int v) {
+    return scan(v, [](int a, int b) { return a + b; });
+}
+__device__ __forceinline__ int scan_max(int v) {
+    return scan(v, [](int a, int b) { return max(a, b); });
 }
 
 // Calls f(Lane, in) for 64 groups at a time, in order, by a whole wave, until it
@@ -50,7 +54,7 @@ __device__ __forceinline__ void for_each(const int32_t* __restrict__ offsets, in
     for (int e0 = 0; e0 < count; e0 += 64) {
         const int e = e0 + lane;
         const bool in = e < count;
-        const int end = scan_max(max(min(in ? offsets[e + 1] : 0, limit), start), lane);
+        const int end = scan_max(max(min(in ? offsets[e + 1] : 0, limit), start));
         const int before = __shfl_up(end, 1);
         Lane g;
         g.e = e;
@@ -58,13 +62,13 @@ __device__ __forceinline__ void for_each(const int32_t* __restrict__ offsets, in
         g.rows = end - g.start;
         g.tiles = (g.rows + T - 1) / T;
         const int words = (g.tiles + 3) >> 2;
-        const int t = scan_add(g.tiles, lane), w = scan_add(words, lane);
+        const int t = scan_add(g.tiles), w = scan_add(words);
         g.tile = tile + t - g.tiles;
         g.word = word + w - words;
         if (f(g, in)) return;
-        start = __shfl(end, 63);
-        tile += __shfl(t, 63);
-        word += __shfl(w, 63);
+        start = __builtin_amdgcn_readlane(end, 63);
+        tile += __builtin_amdgcn_readlane(t, 63);
+        word += __builtin_amdgcn_readlane(w, 63);
     }
 }
 
