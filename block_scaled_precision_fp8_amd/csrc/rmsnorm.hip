@@ -10,8 +10,8 @@
 //
 //   dx = rstd (g - xh mean_k(g xh)) + dh                 dw = sum_rows dy xh
 //
-// dh being the gradient that reaches h along the residual.  Sums are FP32: a lane's
-// columns in order, then across lanes, then across waves, in a fixed order.
+// dh being the gradient that reaches h along the residual.  Sums are FP32, in an order that depends on
+// k alone (dw's on the rows, too): a lane's eight columns, then trees over lanes and pieces.
 //
 // A row is held in registers between its two passes, so each input is read once: HBM
 // bounds the large calls.  Waves take 512 columns at a time, eight per lane: four blocks of
@@ -133,23 +133,35 @@ __device__ __forceinline__ void weight_values(const Raw<WIDE>& r, bool given, in
     else values<WIDE>(r, type, v);
 }
 
-// The sum over a wave, in each of its lanes.
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-    return v;
+// The sum over a wave, in each of its lanes: within quads, mirrored within 8 and 16 lanes, across rows.
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
 }
-// The sum over the `group` waves of a row.  One barrier is enough where calls in turn
-// alternate between two arrays `part`.
-__device__ __forceinline__ float row_sum(float v, float* part, int wave, int group) {
-    v = wave_sum(v);
-    if (group == 1) return v;
-    if ((threadIdx.x & 63) == 0) part[wave] = v;
+__device__ __forceinline__ float wave_sum(float v) {
+    v = add_dpp<0x140>(add_dpp<0x141>(add_dpp<0x4E>(add_dpp<0xB1>(v))));
+    const uint32_t m = __float_as_uint(v);
+    const auto a = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+    const uint32_t n = __float_as_uint(__uint_as_float(a[0]) + __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(n, n, false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+// The sum over a row: each piece's 512 columns, then the pieces, both in a tree that is the same however
+// pieces are spread over waves, so that a row's results do not depend on how many rows a call has.
+// One barrier is enough where calls in turn alternate between two arrays `part`.
+constexpr int kMaxPieces = 64;
+template <int C>
+__device__ __forceinline__ float row_sum(const float (&v)[C], float* part, int wave, int group) {
+    const int lane = threadIdx.x & 63;
+    if (C == 1 && group == 1) return wave_sum(v[0]);
+    part += wave / group * kMaxPieces;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const float s = wave_sum(v[c]);
+        if (lane == 0) part[c * group + wave % group] = s;
+    }
     __syncthreads();
-    const int first = wave / group * group;
-    v = part[first];
-    for (int i = 1; i < group; ++i) v += part[first + i];
-    return v;
+    return wave_sum(lane < C * group ? part[lane] : 0.0f);
 }
 
 struct NormArgs {
@@ -169,7 +181,7 @@ struct NormArgs {
 // X: x's width, R: the residual's, C: pieces of 512 columns per wave.
 template <int X, int R, int FMT, int C>
 __global__ __launch_bounds__(64 * kMaxWaves) void rmsnorm_kernel(NormArgs a) {
-    __shared__ float part[2][kMaxWaves];
+    __shared__ float part[2][4 * kMaxPieces];   // (up to four rows at once)
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int per = (blockDim.x >> 6) / a.group;     // rows at once
@@ -195,8 +207,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void rmsnorm_kernel(NormArgs a) {
             const int64_t col = static_cast<int64_t>(c * a.group + w0) * kWaveColumns + 8 * lane;
             wr[c] = load_weight(a.w, a.w_type, col, a.k - col);
         }
-        float h[C][8];
-        float sum = 0.0f;
+        float h[C][8], part_sum[C] = {};
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int64_t col = static_cast<int64_t>(c * a.group + w0) * kWaveColumns + 8 * lane;
@@ -211,9 +222,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void rmsnorm_kernel(NormArgs a) {
                 if (in) store_raw<R>(a.h, row * a.ldh + col, a.k - col, hr);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum = fmaf(h[c][j], h[c][j], sum);
+            for (int j = 0; j < 8; ++j) part_sum[c] = fmaf(h[c][j], h[c][j], part_sum[c]);
         }
-        sum = row_sum(sum, part[turn], wave, a.group);
+        const float sum = row_sum<C>(part_sum, part[turn], wave, a.group);
         if (!in) continue;
         const float rstd = 1.0f / sqrtf(sum / static_cast<float>(a.k) + a.eps);
         if (a.rstd && w0 == 0 && lane == 0) a.rstd[row] = rstd;
@@ -264,7 +275,7 @@ struct GradArgs {
 // Y: dy's width, H: h's and dx's, A: dh's.
 template <int Y, int H, int A, int C>
 __global__ __launch_bounds__(64 * kMaxWaves) void rmsnorm_grad_kernel(GradArgs a) {
-    __shared__ float part[2][kMaxWaves];
+    __shared__ float part[2][4 * kMaxPieces];   // (up to four rows at once)
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int per = (blockDim.x >> 6) / a.group;
@@ -301,7 +312,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void rmsnorm_grad_kernel(GradArgs a
         const bool in = row < a.rows;
         if constexpr (!AHEAD) fetch(row);
         const float r = rstd;
-        float sum = 0.0f;
+        float part_sum[C] = {};
         float g[C][8], xh[C][8], along[C][8];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -316,11 +327,11 @@ __global__ __launch_bounds__(64 * kMaxWaves) void rmsnorm_grad_kernel(GradArgs a
                 xh[c][j] = there ? xh[c][j] * r : 0.0f;
                 if (in) acc[c][j] = fmaf(g[c][j], xh[c][j], acc[c][j]);
                 g[c][j] = there ? g[c][j] * w[c][j] : 0.0f;
-                sum = fmaf(g[c][j], xh[c][j], sum);
+                part_sum[c] = fmaf(g[c][j], xh[c][j], part_sum[c]);
             }
         }
         if (AHEAD && base + step < a.rows) fetch(row + step);
-        sum = row_sum(sum, part[turn], wave, a.group);
+        const float sum = row_sum<C>(part_sum, part[turn], wave, a.group);
         if (!in) continue;
         const float mean = sum / static_cast<float>(a.k);
 #pragma unroll

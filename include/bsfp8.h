@@ -446,8 +446,8 @@ bsfp8_status scaled_gemm_block128(int64_t M, int64_t N, int64_t K, bsfp8_format 
  * rows >= 0; k at most 32768 (BSFP8_ERR_UNSUPPORTED beyond).  Every array is aligned to
  * its element size, codes to 16 bytes, scales to 4; any other overlap is undefined.
  *
- * FP32 arithmetic, each operation rounded once; the sum of squares in a fixed order, so
- * equal calls give equal bits.  The norm is that of the rounded h, which a backward
+ * FP32 arithmetic, each operation rounded once; the sum of squares in an order that depends on k
+ * alone, so a row gives the same bits in every call.  The norm is that of the rounded h, which a backward
  * pass reads.  Infinities and NaN spread as the formulas have it: a NaN to its row,
  * an infinity (rstd = 0) to itself as NaN, its row otherwise zeros.  Blocks of y with a
  * non-finite value get the scale byte 255 and NaN codes.  rows == 0 or k == 0 writes nothing.
@@ -471,7 +471,7 @@ bsfp8_status rmsnorm_quantize_block128(const void* x, bsfp8_out x_type, int64_t 
  * dimension agree.  dweight: out, FP32 [k], added to what is there with accumulate = 1
  * (0 otherwise); NULL: not wanted.  workspace: rmsnorm_backward_workspace(rows, k) bytes,
  * 16-byte aligned (needed with dweight only); calls that may run at once need one each.
- * FP32 arithmetic, sums in a fixed order.  rows == 0 writes only dweight (zeros, or
+ * FP32 arithmetic, sums in a fixed order (dx's, as the norm's, in one that depends on k alone).  rows == 0 writes only dweight (zeros, or
  * nothing with accumulate); k as in the forward call.
  */
 int64_t rmsnorm_backward_workspace(int64_t rows, int64_t k);

@@ -447,3 +447,56 @@ def test_two_streams_at_once():
             got.append(step(*cases[i % 3]))
     torch.cuda.synchronize()
     assert all(a.equal(c) for i, g in enumerate(got) for a, c in zip(g, want[i % 3]))
+
+
+# ------------------------------------------------------------------ arrays past 2^32 bytes
+def test_rows_past_32_bits():
+    """Codes and outputs of more than 2^32 bytes: the last group's rows against their own small product."""
+    import torch
+    M, N, K, E = 280000, 8192, 64, 3
+    say("grouped: D past 2^32 bytes")
+    o, od = offs([279000, 0, 995], first=2)
+    a = torch.randint(0, 0x7E, (M, K), dtype=torch.uint8, device="cuda")
+    sa = torch.randint(120, 130, (1, M, 4), dtype=torch.uint8, device="cuda")
+    b, sb = (dev(v) for v in weights(E, N, K, "e4m3", 128, 60))
+    d = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    bs.scaled_gemm_grouped_block128(a, sa, b, sb, od, d=d)
+    for e, (p, q) in ((0, (278500, 279002)), (2, (279002, 279997))):
+        want, s = ref.gemm_grouped(from_dev(a[p:q]), from_dev(sa[:, p:q].contiguous()), "e4m3", from_dev(b[e:e + 1]),
+                                   from_dev(sb[e:e + 1]), "e4m3", 128, [0, q - p])
+        check(d[p:q], want, s, "bf16", K, f"rows {p} .. {q - 1}")
+    assert bool((d[:2] == 7.0).all()) and bool((d[279997:] == 7.0).all())
+
+
+def test_weights_past_32_bits():
+    """Experts whose weights lie past 2^32 bytes, in the form for few rows and in a tiled one."""
+    import torch
+    N, K, E = 32768, 49152, 3
+    say("grouped: B past 2^32 bytes")
+    b = torch.randint(0, 0x7E, (E, N, K), dtype=torch.uint8, device="cuda")
+    sb = torch.randint(120, 130, (E, K // 512, N // 128, 4), dtype=torch.uint8, device="cuda")
+    for sizes in ([1, 0, 2], [60, 0, 100]):
+        o, od = offs(sizes)
+        a = torch.randint(0, 0x7E, (int(o[-1]), K), dtype=torch.uint8, device="cuda")
+        sa = torch.randint(120, 130, (K // 512, int(o[-1]), 4), dtype=torch.uint8, device="cuda")
+        d = bs.scaled_gemm_grouped_block128(a, sa, b, sb, od, out="f32")
+        p = int(o[2])
+        f8 = torch.float8_e4m3fn
+        w = b[2, N - 256:].view(f8).double() * torch.exp2(
+            sb[2][:, N // 128 - 2:].transpose(0, 1).reshape(2, -1).double() - 127).repeat_interleave(128, 0).repeat_interleave(128, 1)
+        x = a[p:].view(f8).double() * torch.exp2(
+            sa[:, p:].transpose(0, 1).reshape(sizes[2], -1).double() - 127).repeat_interleave(128, 1)
+        check(d[p:, N - 256:], from_dev(x @ w.t().contiguous()), from_dev(x.abs() @ w.abs().t().contiguous()), "f32", K,
+              f"sizes {sizes}")
+
+
+def test_dispatch_past_32_bits():
+    import torch
+    say("quantize_grouped: x past 2^32 bytes")
+    M, k = 300000, 8192
+    x = torch.randn((M, k), dtype=torch.bfloat16, device="cuda")
+    o, od = offs([100, 50])
+    index = torch.arange(M - 150, M, dtype=torch.int32, device="cuda")
+    got = bs.fp8_quantize_grouped_block128(x, od, "e4m3", index, transposed=True)
+    want = bs.fp8_quantize_grouped_block128(x[M - 150:].contiguous(), od, "e4m3", transposed=True)
+    assert got[0].equal(want[0]) and got[1].equal(want[1]) and got[2][:, :256].equal(want[2][:, :256]) and got[3][:2].equal(want[3][:2])
