@@ -133,6 +133,8 @@ struct GroupsArg {
 // FAST: bf16 output, alpha = 1, without C, every chunk of 8 outputs whole and aligned: the
 // epilogue is then a fixed number of range-checked buffer stores, so the loop
 // can leave them in flight.
+// (Groups' products: any alpha, 16-bit outputs without C or FP32 ones with or without, at
+// any address, any N: the columns past the last whole chunk are stored beside them.)
 //
 // Groups' tiles are counted on the device, from the offsets, so a workgroup first
 // reads those (one wave, 64 groups at a time) into a table in LDS and looks its tiles up there.
@@ -630,11 +632,12 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
                 min(T::ROWS_A, here.end - here.m0) * static_cast<int>(fin.ldc) * es, 0x00020000);
             const uint32_t ld4 = static_cast<uint32_t>(ldd) * es, lc4 = static_cast<uint32_t>(fin.ldc) * es;
             const int row = wm * 32 * TA + srow;
+            const bool edge = (N & 3) && here.n0 + T::ROWS_B > N;
             auto column = [&](int ti) { return nw + 32 * ti + 4 * schunk; };
             u32x4 c[kAhead][4];
             auto fetch_c = [&](auto S) {
                 constexpr int tj = S / TB, ti = S % TB;
-                const uint32_t at = column(ti) < N ? row * lc4 + column(ti) * es : 0x80000000u;
+                const uint32_t at = column(ti) + 4 <= N ? row * lc4 + column(ti) * es : 0x80000000u;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const auto w = __builtin_amdgcn_raw_buffer_load_b128(rs_c, at + (32 * tj + 8 * i) * lc4, 0, 0);
@@ -651,7 +654,7 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
                         make_float4(a[4 * q + 0], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
                 }
                 __builtin_amdgcn_wave_barrier();
-                const uint32_t at = column(ti) < N ? row * ld4 + column(ti) * es : 0x80000000u;
+                const uint32_t at = column(ti) + 4 <= N ? row * ld4 + column(ti) * es : 0x80000000u;
                 u32x4 w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -671,6 +674,21 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     __builtin_amdgcn_raw_buffer_store_b128(w[i], rs_d, at + (32 * tj + 8 * i) * ld4, 0, 0);
+                // the last N % 4 columns, in the lanes of the chunk that they begin (its C is not in w)
+                if (edge) {
+                    const bool mine = column(ti) < N && column(ti) + 4 > N;
+#pragma unroll 1
+                    for (int e = 0; e < (N & 3); ++e)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t o = mine ? (column(ti) + e) * es + row * ld4 : 0x80000000u;
+                            const uint32_t oc = mine ? (column(ti) + e) * es + row * lc4 : 0x80000000u;
+                            float v = __uint_as_float(e == 0 ? w[i][0] : e == 1 ? w[i][1] : w[i][2]);
+                            if (fin.beta != 0.0f)
+                                v = fmaf(fin.beta, __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs_c, oc + (32 * tj + 8 * i) * lc4, 0, 0)), v);
+                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rs_d, o + (32 * tj + 8 * i) * ld4, 0, 0);
+                        }
+                }
                 __builtin_amdgcn_wave_barrier();
             });
         } else if constexpr (FAST) {
@@ -686,8 +704,11 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
 #pragma unroll
             for (int tp = 0; tp < TB / 2; ++tp) {
                 const int col = nw + 64 * tp + 8 * schunk;
-                at[tp] = col < N ? (wm * 32 * TA + srow) * ld2 + col * 2 : 0x80000000u;
+                at[tp] = (KIND == ONE ? col : col + 7) < N ? (wm * 32 * TA + srow) * ld2 + col * 2 : 0x80000000u;
             }
+            // (groups' products take any N: the last N % 8 columns go one by one, beside the count of
+            // stores that the main loop allows for, which may be more)
+            const bool edge = KIND != ONE && (N & 7) && here.n0 + T::ROWS_B > N;
 #pragma unroll
             for (int tj = 0; tj < TA; ++tj)
 #pragma unroll
@@ -711,6 +732,18 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
                         const int R = 8 * i + srow;
                         const u32x4 w = *reinterpret_cast<const u32x4*>(strip + R * 128 + ((schunk ^ ((R >> 1) & 7)) << 4));
                         __builtin_amdgcn_raw_buffer_store_b128(w, rs_d, at[tp] + (32 * tj + 8 * i) * ld2, 0, 0);
+                    }
+                    if (edge) {
+                        const int col = nw + 64 * tp + 8 * schunk;
+                        const uint32_t o = col < N && col + 8 > N ? (wm * 32 * TA + srow) * ld2 + col * 2 : 0x80000000u;
+#pragma unroll 1
+                        for (int e = 0; e < (N & 7); ++e)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int R = 8 * i + srow;
+                                const uint16_t w = *reinterpret_cast<const uint16_t*>(strip + R * 128 + ((schunk ^ ((R >> 1) & 7)) << 4) + 2 * e);
+                                __builtin_amdgcn_raw_buffer_store_b16(w, rs_d, o + 2 * e + (32 * tj + 8 * i) * ld2, 0, 0);
+                            }
                     }
                     __builtin_amdgcn_wave_barrier();
                 }

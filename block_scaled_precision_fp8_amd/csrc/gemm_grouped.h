@@ -6,12 +6,11 @@
 
 namespace bsfp8 {
 
-// What the tiled forms' constant-count epilogue takes: whole 16-byte chunks of D (and C), 32-bit
-// offsets within a tile's rows, and C for FP32 output only.
-inline bool fast_epilogue(int out, int64_t N, const void* d, int64_t ldd, const Epilogue& ep) {
+// What the tiled forms' epilogue by buffer stores takes: 32-bit offsets within a tile's rows, and C for
+// FP32 output only.  Rows of D and C may start at any element (the hardware takes 16 bytes at any address).
+inline bool fast_epilogue(int out, int64_t ldd, const Epilogue& ep) {
     constexpr int64_t most = int64_t(1) << 21;
-    return vec16_ok(out, d, ldd, ep) && N % (out == BSFP8_OUT_F32 ? 4 : 8) == 0 && ldd < most && ep.ldc < most &&
-           (out == BSFP8_OUT_F32 || ep.beta == 0.0f);
+    return ldd < most && ep.ldc < most && (out == BSFP8_OUT_F32 || ep.beta == 0.0f);
 }
 
 // D[i] = alpha A[i] B[e(i)]^T (+ beta C[i]): b and its scales are `groups`
@@ -31,7 +30,7 @@ struct GroupedArgs {
     int64_t ldd;
     Epilogue ep;
     hipStream_t stream;
-    bool fast_ok() const { return fast_epilogue(out, N, d, ldd, ep); }
+    bool fast_ok() const { return fast_epilogue(out, ldd, ep); }
 };
 hipError_t launch_gemm_grouped(const GroupedArgs& t);
 hipError_t launch_gemm_grouped_rows(const GroupedArgs& t);
@@ -56,11 +55,7 @@ struct GroupedKArgs {
     int64_t ldd, d_group, c_group;
     Epilogue ep;
     hipStream_t stream;
-    bool fast_ok() const {
-        const int64_t es = out == BSFP8_OUT_F32 ? 4 : 2;
-        return fast_epilogue(out, N, d, ldd, ep) &&
-               (groups == 1 || ((d_group * es) % 16 == 0 && (ep.beta == 0.0f || (c_group * es) % 16 == 0)));
-    }
+    bool fast_ok() const { return fast_epilogue(out, ldd, ep); }
 };
 hipError_t launch_gemm_grouped_wgrad(const GroupedKArgs& t);
 hipError_t launch_gemm_wgrad_narrow(const GroupedKArgs& t);

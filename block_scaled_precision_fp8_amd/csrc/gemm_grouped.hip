@@ -48,7 +48,7 @@ Form choose_rows(const GroupedArgs& t) {
 // K values by expert.  Narrow: 32 x 32 tiles, three workgroups per CU, K over four waves.
 // 8192 rows of 4 groups, 256 x 256 (narrow, 128 x 128, 256 x 256): 8.6, 17, 35; 300 rows of 8 groups, 256 x 256:
 // 5.3, 7.2, 15; 64 rows of 64 groups, 512 x 512: 81, 17, 22; 2222 rows of 32 groups, 1000 x 2000: 327,
-// 68, 61; 16384 rows of 8 groups, 4096 x 4096: -, 353, 256, and FP32 -, 523, 444.
+// 68, 61 (1000 x 2001: 370, 81, 64); 16384 rows of 8 groups, 4096 x 4096: -, 353, 256, and FP32 -, 523, 444.
 Form choose_columns(const GroupedKArgs& t) {
     const bool wide = t.out == BSFP8_OUT_F32;
     // (columns: the rows in all and up to 127 more per group)

@@ -21,6 +21,7 @@ ROWS = [
     ("T128", "f32", [1999, 129, 0, 2500, 1372], 1004, 1024, "c"),
     ("T256", "bf16", [3001, 0, 257, 2742], 4096, 4096, "plain"),
     ("T256", "f16", [2999, 1, 3000], 4088, 4064, "alpha"),
+    ("T256", "bf16", [2999, 1, 3000], 4093, 4096, "plain"),
 ]
 # form, output, sizes, M, N, epilogue
 COLUMNS = [
@@ -33,11 +34,13 @@ COLUMNS = [
     ("T256", "bf16", [2600, 0, 3401], 2000, 2048, "plain"),
     ("T256", "f16", [129, 3000, 0, 2500], 3900, 4096, "alpha"),
     ("T256", "f32", [3300, 0, 129, 2571], 4096, 4092, "c"),
+    ("T256", "f32", [3300, 0, 129, 2571], 4096, 4091, "c"),
+    ("T256", "bf16", [69] * 20, 1000, 2001, "plain"),
 ]
 
 
 def fast(out, N, epilogue):
-    return N % (4 if out == "f32" else 8) == 0 and (out == "f32" or epilogue != "c")
+    return out == "f32" or epilogue != "c"
 
 
 @pytest.mark.parametrize("form,out,sizes,N,K,epilogue", ROWS)
@@ -140,3 +143,30 @@ def test_columns(form, out, sizes, M, N, epilogue):
             want = s = torch.zeros((M, N), dtype=torch.float64, device="cuda")
         _check(d[e], want, s, out, n + 128, alpha, None if c is None else c[e], f"{label} group {e}")
         col, word = end, last
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_rows_of_outputs_further_apart_than_32_bit_offsets_reach(out):
+    """Row strides of 2^21 elements and more take the epilogue with 64-bit addresses."""
+    import torch
+    ld, sizes, N, K = (1 << 21) + 8, [100, 20, 0, 180, 64, 36], 2052, 992
+    say(f"outputs with a row stride of {ld} elements, {out}")
+    o, od = offs(sizes)
+    M = int(o[-1])
+    assert rows_form(M, N, K, len(sizes), out == "f32", False) == "T64x128"
+    a, sa = bs.fp8_quantize_block128(_random((M, K), 1))
+    w = [bs.fp8_quantize_block128(_random((N, K), 2 + e), "e4m3", 128) for e in range(len(sizes))]
+    b, sb = (torch.stack(t) for t in zip(*w))
+    d = torch.empty((M, ld), dtype=dtype(out), device="cuda")[:, :N]
+    bs.scaled_gemm_grouped_block128(a, sa, b, sb, od, out=out, d=d)
+    assert d.equal(bs.scaled_gemm_grouped_block128(a, sa, b, sb, od, out=out))
+    sizes, M, N = [500, 800], 1300, 900
+    o, od = offs(sizes)
+    columns = bs.lib().block128_grouped_columns(int(o[-1]), 2)
+    assert columns_form(M, N, columns, 2, out == "f32", False) == "T128"
+    x, sx = bs.fp8_quantize_grouped_block128(_random((1300, M), 3), od, rows=False, transposed=True)
+    y, sy = bs.fp8_quantize_grouped_block128(_random((1300, N), 4), od, rows=False, transposed=True)
+    g = torch.empty((2, M, ld), dtype=dtype(out), device="cuda")[:, :, :N]
+    bs.scaled_gemm_grouped_wgrad_block128(x, sx, y, sy, od, out=out, d=g)
+    assert g.equal(bs.scaled_gemm_grouped_wgrad_block128(x, sx, y, sy, od, out=out))
