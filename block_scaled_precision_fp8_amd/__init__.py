@@ -699,6 +699,12 @@ def scaled_gemm_block128(a, a_scales, b, b_scales, a_fmt: str = "e4m3", b_fmt: s
 # ---------------------------------------------------------------------------
 def _matrix(t, name: str, dtypes, device, shape=None):
     """A 2-D tensor (of `shape`) with unit column stride and rows that do not overlap; its row stride."""
+    import torch
+    # what a correct call looks like, in one expression
+    if type(t) is torch.Tensor and t.get_device() == device.index and t.dtype in dtypes and t.is_contiguous():
+        size = t.shape
+        if len(size) == 2 and (shape is None or size == shape):
+            return size[1]
     _tensor(t, name, dtypes, device)
     if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
         raise ValueError(f"{name} must be 2-D{'' if shape is None else f' of shape {tuple(shape)}'}, got {tuple(t.shape)}")
@@ -710,6 +716,9 @@ def _matrix(t, name: str, dtypes, device, shape=None):
 
 
 def _vector(t, name: str, n: int, dtypes, device):
+    import torch
+    if type(t) is torch.Tensor and t.get_device() == device.index and t.dtype in dtypes and t.shape == (n,) and t.is_contiguous():
+        return t
     _tensor(t, name, dtypes, device)
     if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with shape ({n},), got {tuple(t.shape)}")
@@ -853,7 +862,8 @@ def rmsnorm_backward_workspace(rows: int, k: int) -> int:
 def _offsets(offsets, device) -> int:
     """The groups of an int32 tensor of their offsets (groups + 1)."""
     import torch
-    _tensor(offsets, "offsets", (torch.int32,), device)
+    if type(offsets) is not torch.Tensor or offsets.get_device() != device.index or offsets.dtype is not torch.int32:
+        _tensor(offsets, "offsets", (torch.int32,), device)
     if offsets.dim() != 1 or offsets.shape[0] < 1 or not offsets.is_contiguous():
         raise ValueError(f"offsets must be contiguous with groups + 1 elements, got {tuple(offsets.shape)}")
     return offsets.shape[0] - 1
@@ -919,6 +929,9 @@ def fp8_quantize_grouped_block128(x, offsets, fmt: str = "e4m3", index=None, row
 def _bytes(t, name: str, dim: int, device):
     """A contiguous uint8 tensor of `dim` dimensions."""
     import torch
+    if device is not None and type(t) is torch.Tensor and t.get_device() == device.index and t.dtype is torch.uint8 \
+            and t.dim() == dim and t.is_contiguous():
+        return t
     _tensor(t, name, (torch.uint8,), device)
     if t.dim() != dim or not t.is_contiguous():
         raise ValueError(f"{name} must be {dim}-D and contiguous, got shape {tuple(t.shape)}")
@@ -932,6 +945,7 @@ def scaled_gemm_grouped_block128(a, a_scales, b, b_scales, offsets, a_fmt: str =
     offsets[e] .. offsets[e + 1] - 1 (int32, on the device).  a: M x K codes with scales per
     1 x 128 block; b: [groups, N, K] codes, b_scales [groups, *block128_scale_shape(N, K, b_block_rows)].
     Rows of no group are left as they were.  c may be d itself."""
+    import torch
     fa, fb = _fp8_fmt(a_fmt), _fp8_fmt(b_fmt)
     _block_rows(b_block_rows, "b_block_rows")
     _bytes(a, "a", 2, None)
@@ -943,13 +957,18 @@ def scaled_gemm_grouped_block128(a, a_scales, b, b_scales, offsets, a_fmt: str =
     (M, K), N = a.shape, b.shape[1]
     if b.shape[0] != groups or b.shape[2] != K:
         raise ValueError(f"b must be {groups} x N x {K}, got {tuple(b.shape)}")
-    if a_scales.shape != block128_scale_shape(M, K, 1):
+    words = (K + 511) // 512
+    if a_scales.shape != (words, M, 4):
         raise ValueError(f"a_scales must have shape {block128_scale_shape(M, K, 1)}, got {tuple(a_scales.shape)}")
-    if b_scales.shape != (groups, *block128_scale_shape(N, K, b_block_rows)):
+    if b_scales.shape != (groups, words, (N + b_block_rows - 1) // b_block_rows, 4):
         raise ValueError(f"b_scales must have shape {(groups, *block128_scale_shape(N, K, b_block_rows))}, "
                          f"got {tuple(b_scales.shape)}")
     given = d is not None
-    d, cp, ldc = _epilogue_tensors(d, c, beta, M, N, out, dev)
+    if not given and c is None and beta == 0.0:
+        _key(OUTS, out, "output type")
+        d, cp, ldc = torch.empty((M, N), dtype=getattr(torch, _OUT_DTYPES[out]), device=dev), 0, 0
+    else:
+        d, cp, ldc = _epilogue_tensors(d, c, beta, M, N, out, dev)
     if M and N and groups:
         st = _call(dev, lib().scaled_gemm_grouped_block128, M, N, K, groups, offsets.data_ptr(), fa, a.data_ptr(),
                    a_scales.data_ptr(), fb, b.data_ptr(), b_scales.data_ptr(), b_block_rows, alpha, cp, ldc, beta,
