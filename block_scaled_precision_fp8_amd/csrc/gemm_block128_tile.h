@@ -269,11 +269,12 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
     auto advance = [&]() {
         if (++l_stage == l_stages) {
             l_stage = 0;
+            // the search and the lookup are the compiler's code, which may move what it takes as
+            // written: no fragment may still be on its way to a register
+            lds_wait();
             l_tile = next_tile(l_tile + gridDim.x, gridDim.x);
             const bool any = l_tile < last;
             Place p{};
-            // (the lookup is the compiler's code: no fragment may still be on its way to a register)
-            if constexpr (KIND != ONE) lds_wait();
             if (any) p = locate(l_tile);
             if constexpr (KIND == COLUMNS) l_stages = stages(p);
             aim(p, any);
@@ -436,6 +437,8 @@ __global__ __launch_bounds__(kThreads, (Tile<TA, TB>::PERSISTENT ? 1 : 2)) void 
     static_for<TA + TB>([&](auto I) { read_scale(I, 0); });
     if constexpr (!WIDE) {
         static_for<T::NR>([&](auto R) { read_one(R, fr[0], C0, C0); });
+        // (the lookup of the next tile follows: as in advance)
+        lds_wait();
     } else {
         static_for<TA + TB>([&](auto R) { read_half(R, hs[0], C0, C0); });
         static_for<TA + TB>([&](auto R) { read_half(R, hs[1], C0, C1); });
