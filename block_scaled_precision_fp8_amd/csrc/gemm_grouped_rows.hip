@@ -70,6 +70,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gemm_grouped_rows_kernel(
                     acc = block_product<AF, BF, OUT, j>(b[2 * j], b[2 * j + 1], a[2 * j], a[2 * j + 1], wb, wa, acc);
                 });
             }
+            // A matrix instruction's result may be read some cycles after its issue only.  This compiler leaves those
+            // out behind a loop that may be skipped: the first of each four columns came out wrong.
+            asm volatile("s_nop 15" : "+v"(acc));
             part[wave][lane] = acc;
             __syncthreads();
             if (wave == 0) {
