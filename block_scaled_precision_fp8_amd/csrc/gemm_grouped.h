@@ -63,6 +63,10 @@ hipError_t launch_gemm_wgrad_4x4(const GroupedKArgs& t);           // 16-bit out
 hipError_t launch_gemm_wgrad_4x4_f32(const GroupedKArgs& t);
 hipError_t launch_gemm_wgrad_2x2(const GroupedKArgs& t);
 
+// Which form a call runs on (0 few rows or 32 x 32 tiles, 1 64 x 128, 2 128 x 128, 3 256 x 256), for the tests.
+int gemm_grouped_form(int64_t M, int64_t N, int64_t K, int groups, int out, int64_t ldd, int64_t ldc, float beta);
+int gemm_wgrad_form(int64_t M, int64_t N, int64_t columns, int groups, int out, int64_t ldd, int64_t ldc, float beta);
+
 // finish_row_chunk for four columns at any alignment: a whole chunk moves in one access (the hardware
 // takes any element's address).  With D of 2001 columns 32 products 1000 x 2001 x 69 took
 // 106 us element by element, 81 so.

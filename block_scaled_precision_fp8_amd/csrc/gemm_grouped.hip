@@ -13,12 +13,17 @@ namespace {
 enum Form { FEW, T64x128, T128, T256 };
 
 // Rows by expert.  A tiled form runs `stage` per 128 K and tile on each CU, and `tile` besides; the
-// form for few rows moves 32 bytes per K and 16 x 16 tile at 10 TB/s; every form reads the
-// weights of the groups that have rows at 5 TB/s, which hides behind the products by some 70%.
+// form for few rows moves 32 bytes per K and 16 x 16 tile at 10 TB/s.  The weights of the groups that have rows
+// are read at 5 TB/s (6 by the form for few rows), which hides behind the tiled products by some 70%.
 // 64 groups, N 2048, K 4096, 16-bit output (few rows, 64 x 128, 128 x 128, 256 x 256): 128 rows 73, 97, 101,
 // 108; 512 rows 118, 120, 123, 126; 1024 rows 172, 122, 127, 130; 4096 rows 545, 130, 147, 167; 8192
 // rows 1019, 160, 150, 174; 16384 rows 2005, 238, 204, 176.  16384 rows of 8 groups, N 14336: -,
 // 1334, 1037, 770; 8 rows of 16 groups, N 1024: 8.6, 15.9, 17.2, 37.4.
+// With few columns the form for few rows has few workgroups, each of which walks its group's 16-row tiles one after
+// another, at 0.25 us and 1 us per 1024 K each (K 512: 0.75 to 0.9, K 4096: 4.3): the largest group, taken as
+// twice the mean, sets the time, the first tile being in the 4 us of every form.  N 16, K 4096 (few rows,
+// 64 x 128): 2 groups of 64 rows 21, 12.2; 8 of 16 rows 8.9, 12.3; 8 of 64 rows 21.5, 12.4; 64 of 8 rows 5.8, 12.3; 64 of
+// 32 rows 15.6, 14.8; 8 of 2048 rows 557, 19.3; K 512: 8 of 16 rows 2.9, 4.4; 8 of 64 rows 5.3, 4.4; 2 of 1024 rows 50, 4.5.
 Form choose_rows(const GroupedArgs& t) {
     const bool wide = t.out == BSFP8_OUT_F32;
     const double M = static_cast<double>(t.M), N = static_cast<double>(t.N), K = static_cast<double>(t.K);
@@ -28,7 +33,8 @@ Form choose_rows(const GroupedArgs& t) {
     auto total = [&](double products) { return 4.0 + std::max(weights, products) + 0.3 * std::min(weights, products); };
     Form form = FEW;
     // (a workgroup of up to 1024 threads per 16 columns and group; threads are counted in 32 bits)
-    double best = 4.0 + std::max(groups * N * K / 6.0e6, row_tiles(16) * (N / 16.0) * K * 32.0 / 10.0e6);
+    const double walk = std::max(0.0, 2.0 * M / groups / 16.0 - 1.0) * (0.25 + K / 1024.0);
+    double best = 4.0 + std::max({groups * N * K / 6.0e6, row_tiles(16) * (N / 16.0) * K * 32.0 / 10.0e6, walk});
     if ((t.N + 15) / 16 * t.groups >= int64_t(1) << 22) best = 1e300;
     struct Cost { Form form; int rows, columns; double stage, stage_f32, tile; };
     static constexpr Cost kCost[3] = {{T64x128, 64, 128, 0.37, 0.51, 0.0}, {T128, 128, 128, 0.56, 0.88, 0.0}, {T256, 256, 256, 1.35, 1e9, 8.0}};
@@ -75,6 +81,18 @@ hipError_t launch_gemm_grouped(const GroupedArgs& t) {
     case T256: return launch_gemm_grouped_4x4(t);
     default: return launch_gemm_grouped_rows(t);
     }
+}
+
+int gemm_grouped_form(int64_t M, int64_t N, int64_t K, int groups, int out, int64_t ldd, int64_t ldc, float beta) {
+    GroupedArgs t{};
+    t.M = M, t.N = N, t.K = K, t.groups = groups, t.out = out, t.ldd = ldd, t.ep.ldc = ldc, t.ep.beta = beta;
+    return K == 0 ? FEW : choose_rows(t);
+}
+
+int gemm_wgrad_form(int64_t M, int64_t N, int64_t columns, int groups, int out, int64_t ldd, int64_t ldc, float beta) {
+    GroupedKArgs t{};
+    t.M = M, t.N = N, t.columns = columns, t.groups = groups, t.out = out, t.ldd = ldd, t.ep.ldc = ldc, t.ep.beta = beta;
+    return choose_columns(t);
 }
 
 hipError_t launch_gemm_grouped_wgrad(const GroupedKArgs& t) {
