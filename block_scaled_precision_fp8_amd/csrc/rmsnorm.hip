@@ -149,6 +149,17 @@ __device__ __forceinline__ float add_dpp(float v) {
 __device__ __forceinline__ float wave_sum(float v) {
     return add_rows(add_dpp<0x140>(add_dpp<0x141>(add_dpp<0x4E>(add_dpp<0xB1>(v)))));
 }
+// v^(-1/2), rounded once (to within 2^-18 of a step): the hardware's estimate r, off by up to a step and not
+// made for subnormal v, moved by r (1 - v r^2) / 2, that difference formed from the exact product v r.
+// 1 / sqrt(v), which rounds twice, is another value than the nearest one for a quarter of all v.
+__device__ __forceinline__ float reciprocal_root(float v) {
+    const bool tiny = v < 0x1p-100f;
+    const float e = __builtin_amdgcn_rsqf(tiny ? v * 0x1p100f : v), r = tiny ? e * 0x1p50f : e;
+    const float t = v * r, low = fmaf(v, r, -t);
+    const float off = fmaf(-low, r, fmaf(-t, r, 1.0f));
+    // (zero and infinity have theirs already, and NaN stays)
+    return r > 0.0f && r < INFINITY ? fmaf(0.5f * r, off, r) : r;
+}
 // The sum over a row: each piece's 512 columns, then the pieces, both in a tree that is the same however
 // pieces are spread over waves, so that a row's results do not depend on how many rows a call has.
 // One barrier is enough where calls in turn alternate between two arrays `part`.
@@ -229,7 +240,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void rmsnorm_kernel(NormArgs a) {
         }
         const float sum = row_sum<C>(part_sum, part[turn], wave, a.group);
         if (!in) continue;
-        const float rstd = 1.0f / sqrtf(sum / static_cast<float>(a.k) + a.eps);
+        const float rstd = reciprocal_root(sum / static_cast<float>(a.k) + a.eps);
         if (a.rstd && w0 == 0 && lane == 0) a.rstd[row] = rstd;
 #pragma unroll
         for (int c = 0; c < C; ++c) {

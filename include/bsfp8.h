@@ -446,7 +446,7 @@ bsfp8_status scaled_gemm_block128(int64_t M, int64_t N, int64_t K, bsfp8_format 
  * rows >= 0; k at most 32768 (BSFP8_ERR_UNSUPPORTED beyond).  Every array is aligned to
  * its element size, codes to 16 bytes, scales to 4; any other overlap is undefined.
  *
- * FP32 arithmetic, each operation rounded once; the sum of squares in an order that depends on k
+ * FP32 arithmetic, each operation (the reciprocal root is one) rounded once; the sum of squares in an order that depends on k
  * alone, so a row gives the same bits in every call.  The norm is that of the rounded h, which a backward
  * pass reads.  Infinities and NaN spread as the formulas have it: a NaN to its row,
  * an infinity (rstd = 0) to itself as NaN, its row otherwise zeros.  Blocks of y with a
