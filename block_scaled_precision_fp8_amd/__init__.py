@@ -66,8 +66,11 @@ def lib() -> ctypes.CDLL:
             "`python -c 'import __graft_entry__ as g; g.build()'` or "
             "`python block_scaled_precision_fp8_amd/build.py`")
     # torch brings a HIP runtime of its own; loaded after this library's, it would be a second one in
-    # the process, and launches on its streams would fail
-    import torch  # noqa: F401
+    # the process, and launches on its streams would fail.  (The C functions do without torch.)
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        pass
     L = ctypes.CDLL(LIB_PATH)
     i64, vp, c_int = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
     L.fp8_quantize.argtypes = [vp, i64, i64, i64, c_int, c_int, vp, vp, vp]
