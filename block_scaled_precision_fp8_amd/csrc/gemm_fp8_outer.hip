@@ -287,6 +287,9 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_fp8_outer_kernel(
                 });
             }
         });
+        // The last products settle here, while the matrix core is at them anyway: where the loop ends the
+        // compiler may copy an accumulator ahead of the wait below.
+        if constexpr (OUT != BSFP8_OUT_F32) asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 3" ::: "memory");
     }
     // no direct load may still be writing LDS when the epilogue reuses it, and
     // the last step's fragment reads, which have no consumer, are named after

@@ -920,6 +920,9 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_mxfp4_ring_kernel(
                 }
             });
         });
+        // The last products settle here, while the matrix core is at them anyway: where the loop ends the
+        // compiler may copy an accumulator ahead of the wait below.
+        asm volatile("s_nop 7\n\ts_nop 3" ::: "memory");
     }
     // no direct load may still be writing LDS when the workgroup ends, and no
     // register load may still be in flight when its register is reused: the
