@@ -561,10 +561,11 @@ __global__ __launch_bounds__(QA ? kQThreads : kThreads, QA ? 1 : 2) void gemm_fp
     // the last full block's pending tile
     promote(acc[1][1], pend_sig, pend);
     if (nfull < nst) {
-        // partial stage: its data and block-0 fragments are already in place
+        // partial stage: its data and block-0 fragments are already in place (and waited for here,
+        // since the compiler may copy them as soon as the stages have ended)
         const int cb = nfull & 1;
-        if constexpr (QA) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
-        else asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+        if constexpr (QA) asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)" ::: "memory");
+        else asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)" ::: "memory");
         u32x4 ca = nsa, cbv = nsb;
         asm volatile("" : "+v"(ca), "+v"(cbv));
         const int nk = nkb - 4 * nfull;

@@ -401,8 +401,9 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_fp8_big_kernel(
 
     if (nfull < nst) {
         // partial stage (1 to 3 blocks) in buffer nfull % 2: its scales and
-        // block 0's A and first B fragments are already loaded (set 0)
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        // block 0's A and first B fragments are already loaded (set 0; waited for here, since the
+        // compiler may copy them as soon as the stages have ended)
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         u32x4 ca = nsa, cbv = nsb;
         asm volatile("" : "+v"(ca), "+v"(cbv));
         const int nk = nkb - 4 * nfull;

@@ -242,7 +242,7 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_fp8_outer_kernel(
             // fragments are in registers), which stage s + 4 then refills
             asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
             lds_wait_barrier();
-            const Frag& f = fr[u & 1];
+            Frag& f = fr[u & 1];
             Frag& g = fr[(u + 1) & 1];
             constexpr auto nbuf = std::integral_constant<int, (u + 1) & 3>{};
             if constexpr (OUT != BSFP8_OUT_F32) {
@@ -262,6 +262,12 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_fp8_outer_kernel(
                 // (24 fraction bits).  Each lane's 32 codes of a step form four
                 // groups of 8 (K positions in the same order on both operands,
                 // so every product still pairs equal K).
+                // (The fragments are named after the wait: the conversions are the compiler's code, which
+                // it moves ahead of it otherwise.)
+                asm volatile("" : "+v"(f.xl[0]), "+v"(f.xl[1]), "+v"(f.xl[2]), "+v"(f.xl[3]),
+                                  "+v"(f.xh[0]), "+v"(f.xh[1]), "+v"(f.xh[2]), "+v"(f.xh[3]));
+                asm volatile("" : "+v"(f.yl[0]), "+v"(f.yl[1]), "+v"(f.yl[2]), "+v"(f.yl[3]),
+                                  "+v"(f.yh[0]), "+v"(f.yh[1]), "+v"(f.yh[2]), "+v"(f.yh[3]));
                 static_for<4>([&](auto I) {
                     constexpr int i = I;
                     u32x4 xw[4], yw[4];
@@ -290,6 +296,7 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_fp8_outer_kernel(
         // The last products settle here, while the matrix core is at them anyway: where the loop ends the
         // compiler may copy an accumulator ahead of the wait below.
         if constexpr (OUT != BSFP8_OUT_F32) asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 3" ::: "memory");
+        else asm volatile("s_nop 7\n\ts_nop 3" ::: "memory");
     }
     // no direct load may still be writing LDS when the epilogue reuses it, and
     // the last step's fragment reads, which have no consumer, are named after

@@ -575,8 +575,10 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_mxfp4_big_kernel(
             constexpr int nks = (ks + 1) & 3;
             constexpr int NM = 16 * SUB;          // MFMAs of the step
             constexpr int LD = 2 * SUB;           // MFMAs per direct load
-            const Frag& f = fr[ks & 1];
+            Frag& f = fr[ks & 1];
             Frag& g = fr[(ks + 1) & 1];
+            // (named after the wait: parts of A's fragments are copied below, by the compiler's code)
+            if constexpr (SUB != 1) asm volatile("" : "+v"(f.y[0]), "+v"(f.y[1]), "+v"(f.y[2]), "+v"(f.y[3]));
             const int rb = ks == 3 ? cb ^ 1 : cb;
             const uint32_t ra_addr = rb ? rd_a[1][nks] : rd_a[0][nks];
             const uint32_t rb_addr = rb ? rd_b[1][nks] : rd_b[0][nks];
@@ -639,6 +641,8 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_mxfp4_big_kernel(
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         lds_wait_barrier();
         kstep(std::integral_constant<int, 3>{});
+        // (where the loop ends the compiler may copy the fragments: they are here then)
+        lds_wait();
     };
     int s0 = 0;
     for (; s0 + 1 < nst; s0 += 2) {

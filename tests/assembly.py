@@ -1,8 +1,8 @@
 """Checks of the built library's gfx950 code, over the control flow of each kernel, for what the hardware leaves to
-software: how soon a matrix instruction's result may be used.
+software: how soon a matrix instruction's result may be used, and that a read from LDS has arrived.
 
-The compiler sees to that for its own instructions, but not where inline assembly is a side; and it has been seen
-to leave it out behind a loop that may be skipped.
+The compiler sees to both for its own instructions, but not where inline assembly is a side; and it has been seen
+to leave the first out behind a loop that may be skipped.
 """
 import glob
 import os
@@ -128,3 +128,32 @@ def early_uses(code):
 
     _flow(code, step, lambda a, b: need(a[1]) - a[0] > need(b[1]) - b[0])
     return sorted(found.values())
+
+def unfinished_reads(code):
+    """(the read, the instruction that uses its registers) where nothing waited for a read from LDS."""
+    found = set()
+
+    def step(entry, body):
+        # register -> (how many LDS operations were issued after its read, the read)
+        live = dict(entry)
+        for ins in body:
+            op, _, rest = ins.partition(" ")
+            if op == "s_waitcnt":
+                m = re.search(r"lgkmcnt\((\d+)\)", rest)
+                if m:
+                    live = {r: v for r, v in live.items() if v[0] < int(m.group(1))}
+                continue
+            if op.startswith(_VECTOR):
+                for r in registers(rest):
+                    if r in live:
+                        found.add((live[r][1], ins))
+                        del live[r]
+            if op.startswith(("ds_", "s_load", "s_buffer_load", "flat_")):
+                live = {r: (n + 1, read) for r, (n, read) in live.items()}
+            if op.startswith(("ds_read", "ds_bpermute", "ds_permute", "ds_swizzle")):
+                for r in registers(rest.split(",")[0] if "[" not in rest.split(",")[0] else rest[:rest.index("]") + 1]):
+                    live[r] = (0, ins)
+        return live
+
+    _flow(code, step, lambda a, b: a[0] < b[0])
+    return sorted(found)

@@ -4,12 +4,12 @@ import concurrent.futures
 import pytest
 
 import block_scaled_precision_fp8_amd as bs
-from assembly import disassemble, early_uses, kernels
+from assembly import disassemble, early_uses, kernels, unfinished_reads
 
 
 def _check(text):
-    """Per kernel with matrix instructions: its name and the uses of results that come too soon."""
-    return [(name, early_uses(code)) for name, code in kernels(text) if any("v_mfma" in ins for _, ins, _ in code)]
+    """Per kernel with matrix instructions: its name, the uses of results that come too soon and of LDS reads not waited for."""
+    return [(name, early_uses(code), unfinished_reads(code)) for name, code in kernels(text) if any("v_mfma" in ins for _, ins, _ in code)]
 
 
 @pytest.fixture(scope="module")
@@ -21,8 +21,13 @@ def checked(tmp_path_factory):
 
 def test_results_are_not_used_too_soon(checked):
     assert len(checked) > 300
-    for name, early in checked:
+    for name, early, _ in checked:
         assert not early, f"{name}: {len(early)} uses, the first after {early[0][0]} of {early[0][1]} wait states: {early[0][2]} | {early[0][3]}"
+
+
+def test_reads_from_lds_have_arrived(checked):
+    for name, _, reads in checked:
+        assert not reads, f"{name}: {len(reads)} uses of reads in flight: {reads[0][0]} | {reads[0][1]}"
 
 
 def code_of(text):
@@ -71,3 +76,22 @@ def test_the_count_knows_the_instructions():
     # another register, a result overwritten in between, and the next product's accumulator are no uses
     assert not uses(fp8, 2, "v_accvgpr_read_b32 v40, a16") and not uses(fp8, 2, fp8)
     assert uses(fp8, 2, "v_mfma_f32_32x32x16_bf16 a[16:31], a[0:3], v[8:11], a[16:31]") == [(2, 20)]
+
+
+@pytest.mark.parametrize("wait,reads", [("lgkmcnt(0)", 0), ("lgkmcnt(1)", 0), ("lgkmcnt(2)", 1), ("vmcnt(0)", 1), ("vmcnt(3) lgkmcnt(0)", 0)])
+def test_the_reads_are_counted_in_order(wait, reads):
+    """Of three LDS operations the second is waited for, or not, and used around a loop."""
+    text = f"""ds_read_b32 v1, v0
+head:
+ds_read_b128 v[4:7], v0 offset:16
+ds_write_b32 v0, v9
+s_waitcnt {wait}
+v_add_u32_e32 v10, v10, v6
+s_cbranch_scc0 head
+s_endpgm"""
+    assert len({r for r, _ in unfinished_reads(code_of(text))}) == reads
+
+
+def test_a_register_written_over_a_read_in_flight_counts():
+    assert unfinished_reads(code_of("ds_read_b64 v[4:5], v0\nv_mov_b32_e32 v5, 0\ns_endpgm"))
+    assert not unfinished_reads(code_of("ds_read_b64 v[4:5], v0\nv_mov_b32_e32 v6, 0\ns_waitcnt lgkmcnt(0)\nv_mov_b32_e32 v5, v4\ns_endpgm"))
