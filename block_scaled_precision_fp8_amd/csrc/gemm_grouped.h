@@ -1,4 +1,8 @@
 // gemm_grouped.h -- shared by the forms of the grouped block-of-128 FP8 products.
+//
+// Products are summed as in the ungrouped product: for 16-bit outputs by the FP8 matrix instruction, twice as fast as
+// bf16's, which keeps 13 fraction bits within a group of products (up to 7 2^-13 of sum |a b|, about 2% of bf16 outputs
+// one step from those of FP32 sums); for FP32 output in bf16, which is exact for the codes.
 #pragma once
 
 #include "gemm_block128.h"

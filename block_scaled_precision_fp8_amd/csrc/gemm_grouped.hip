@@ -1,7 +1,8 @@
 // gemm_grouped.hip -- which form a grouped block-of-128 FP8 product runs on (gfx950).
 //
 // The groups' sizes are on the device, so the choice goes by their number and the rows in all: as if
-// the rows were spread evenly, half a tile of each group empty.  Times are microseconds on MI355X.
+// the rows were spread evenly, half a tile of each group empty.  Times are microseconds on MI355X, of calls
+// in a captured graph.
 #include "gemm_grouped.h"
 
 #include <algorithm>
@@ -15,10 +16,10 @@ enum Form { FEW, T64x128, T128, T256 };
 // Rows by expert.  A tiled form runs `stage` per 128 K and tile on each CU, and `tile` besides; the
 // form for few rows moves 32 bytes per K and 16 x 16 tile at 10 TB/s.  The weights of the groups that have rows
 // are read at 5 TB/s (6 by the form for few rows), which hides behind the tiled products by some 70%.
-// 64 groups, N 2048, K 4096, 16-bit output (few rows, 64 x 128, 128 x 128, 256 x 256): 128 rows 73, 97, 101,
-// 108; 512 rows 118, 120, 123, 126; 1024 rows 172, 122, 127, 130; 4096 rows 545, 130, 147, 167; 8192
-// rows 1019, 160, 150, 174; 16384 rows 2005, 238, 204, 176.  16384 rows of 8 groups, N 14336: -,
-// 1334, 1037, 770; 8 rows of 16 groups, N 1024: 8.6, 15.9, 17.2, 37.4.
+// 64 groups, N 2048, K 4096, 16-bit output (few rows, 64 x 128, 128 x 128, 256 x 256): 128 rows 84, 110, 113,
+// 116; 512 rows 106, 123, 127, 129; 1024 rows 164, 124, 127, 130; 4096 rows 520, 136, 131, 135; 8192
+// rows 991, 168, 151, 143; 16384 rows 1941, 256, 205, 188.  16384 rows of 8 groups, N 14336: -,
+// 1440, 1039, 763; 8 rows of 16 groups, N 1024: 8.7, 15.5, 16.9, 37.0.
 // With few columns the form for few rows has few workgroups, each of which walks its group's 16-row tiles one after
 // another, at 0.25 us and 1 us per 1024 K each (K 512: 0.75 to 0.9, K 4096: 4.3): the largest group, taken as
 // twice the mean, sets the time, the first tile being in the 4 us of every form.  N 16, K 4096 (few rows,
@@ -52,9 +53,11 @@ Form choose_rows(const GroupedArgs& t) {
 }
 
 // K values by expert.  Narrow: 32 x 32 tiles, three workgroups per CU, K over four waves.
-// 8192 rows of 4 groups, 256 x 256 (narrow, 128 x 128, 256 x 256): 8.6, 17, 35; 300 rows of 8 groups, 256 x 256:
-// 5.3, 7.2, 15; 64 rows of 64 groups, 512 x 512: 81, 17, 22; 2222 rows of 32 groups, 1000 x 2000: 327,
-// 68, 61 (1000 x 2001: 370, 81, 64); 16384 rows of 8 groups, 4096 x 4096: -, 353, 256, and FP32 -, 523, 444.
+// 8192 rows of 4 groups, 256 x 256 (narrow, 128 x 128, 256 x 256): 7.4, 12.4, 24.9; 300 rows of 8 groups, 256 x 256:
+// 4.4, 5.1, 9.6; 64 rows of 64 groups, 512 x 512: 71, 17, 21; 2222 rows of 32 groups, 1000 x 2000: 287,
+// 69, 60 (1000 x 2001: 294, 72, 64); 16384 rows of 8 groups, 4096 x 4096: -, 344, 245, and FP32 -, 521, 445 (with
+// C -, 590, 535).  Over 120 sizes (128 to 8192 rows of 1 to 32 groups, 256 x 256 to 4096 x 1024) the choice is within 13% of
+// the best form, but for one long group: 8192 rows, 1000 x 2000, FP32 runs narrow, 83 where 128 x 128 takes 53.
 Form choose_columns(const GroupedKArgs& t) {
     const bool wide = t.out == BSFP8_OUT_F32;
     // (columns: the rows in all and up to 127 more per group)

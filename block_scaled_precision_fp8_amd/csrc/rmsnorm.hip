@@ -402,6 +402,12 @@ __global__ __launch_bounds__(64 * kMaxWaves) void column_sum_kernel(const float*
 // rows per workgroup at once, `grid` workgroups.
 struct Spread { int pieces, group, per, grid; };
 
+// One piece per wave spreads a row over the most waves, which small calls need; more rows in flight per
+// workgroup suit large ones.  bf16 with residual (one piece, two, four): 16 x 8192 5.3, 5.2, 6.8 us; 512 x 4096
+// 6.2, 6.3, 8.1; 512 x 8192 12.0, 10.2, 12.1; 1024 x 8192 21.6, 16.2, 16.6; 2048 x 4096 17.2, 16.1, 16.5;
+// 16384 x 4096 99.8, 87.5, 94.2; 16384 x 8192 284, 175, 179; of up to 2048 columns 2048 x 2048 10.1, 10.1,
+// 12.0, 16384 x 2048 49.0, 43.1, 48.4.  (Two, four): 2048 x 12288 38, 55; 2048 x 16384 60, 55.  Beyond
+// 16384 columns a workgroup's 16 waves need four.
 Spread norm_spread(int64_t rows, int64_t k) {
     const int n = static_cast<int>((k + kWaveColumns - 1) / kWaveColumns);
     const int pieces = n <= 4 || (n <= kMaxWaves && rows <= 512) ? 1 : n <= 2 * kMaxWaves ? 2 : 4;
@@ -415,8 +421,14 @@ Spread grad_spread(int64_t rows, int64_t k) {
     const int pieces = n <= kMaxWaves ? 1 : n <= 2 * kMaxWaves ? 2 : 4;
     const int group = (n + pieces - 1) / pieces, per = group >= 4 ? 1 : 4 / group;
     // Each workgroup writes a partial row of dw: two per CU where rows are many, else one, and as few as
-    // give each the same number of rows.  16384 x 4096 bf16 with dh: 96.9 us with up to 512 workgroups, 100.3
-    // with 256; 777 x 5001 FP32: 27.4 and 22.6.
+    // give each the same number of rows.  bf16 without dh (256 workgroups, 512): 777 x 4096 12.2, 13.1 us;
+    // 2500 x 4096 19.9, 21.4; 3500 x 4096 24.3, 24.6; 4096 x 4096 26.3, 25.1; 16384 x 4096 75.3, 70.7;
+    // 16384 x 5001 199, 143.  FP32: 2500 x 5001 45.0, 44.3; 6000 x 5001 94.8, 87.5.  (With 8192 columns and
+    // more one per CU stays ahead up to 6000 rows: 6000 x 8192 56, 64.)
+    // Pieces as few as fit: two in place of one took 4096 x 4096 from 25 to 36 us, four in place of two
+    // 4096 x 12288 from 80 to 179.  With two and more there is no look-ahead, and four spill (58 to 212
+    // registers, at the 128 of a workgroup of 16 waves): rows past 8192 columns run, but not near the time of
+    // their bytes (1500 x 20001 bf16 131 us, 37 at a copy's rate).
     const int64_t groups = (rows + per - 1) / per, most = rows >= 4096 ? 512 : 256, turns = (groups + most - 1) / most;
     return {pieces, group, per, static_cast<int>(turns ? (groups + turns - 1) / turns : 0)};
 }

@@ -449,7 +449,8 @@ bsfp8_status scaled_gemm_block128(int64_t M, int64_t N, int64_t K, bsfp8_format 
  * FP32 arithmetic, each operation (the reciprocal root is one) rounded once; the sum of squares in an order that depends on k
  * alone, so a row gives the same bits in every call.  The norm is that of the rounded h, which a backward
  * pass reads.  Infinities and NaN spread as the formulas have it: a NaN to its row,
- * an infinity (rstd = 0) to itself as NaN, its row otherwise zeros.  Blocks of y with a
+ * an infinity (rstd = 0) to itself as NaN, its row otherwise zeros (a row whose squares add
+ * up past FP32's range is zeros likewise).  Blocks of y with a
  * non-finite value get the scale byte 255 and NaN codes.  rows == 0 or k == 0 writes nothing.
  */
 bsfp8_status rmsnorm_quantize_block128(const void* x, bsfp8_out x_type, int64_t rows, int64_t k, int64_t ldx,
@@ -511,6 +512,8 @@ bsfp8_status rmsnorm_backward(const void* dy, bsfp8_out dy_type, int64_t ldy, co
  * columns, words: a multiple of 128 and a count, at least what
  *         block128_grouped_columns(rows, groups) and block128_grouped_words(rows, groups) return
  *         (enough for any sizes of so many groups).
+ * At most 2^23 tiles of 128 x 128 (columns / 128 * ceil(k / 128)) with the transpose, 2^27 pieces of 512
+ * (rows * ceil(k / 512)) without.
  */
 int64_t block128_grouped_columns(int64_t rows, int64_t groups);
 int64_t block128_grouped_words(int64_t rows, int64_t groups);
@@ -529,7 +532,7 @@ bsfp8_status fp8_quantize_grouped_block128(const void* x, bsfp8_out x_type, int6
  * ceil(N / 128) for b_block_rows 1 or 128.  alpha, c, ldc, beta, out, d, ldd, the
  * limits on N and K and the accuracy: as for scaled_gemm_block128.  At most 2^24 - 16 tiles of
  * 64 x 128 ((M / 64 + groups) ceil(N / 128)).  The kernel form is chosen by the sizes, the
- * number of groups and the output alone: equal calls give equal bits.
+ * number of groups, the output type, ldd, ldc and whether beta is 0: equal calls give equal bits.
  */
 bsfp8_status scaled_gemm_grouped_block128(int64_t M, int64_t N, int64_t K, int64_t groups, const int32_t* offsets,
                                           bsfp8_format a_fmt, const void* a, const void* a_scales, bsfp8_format b_fmt,
